@@ -61,7 +61,7 @@ typedef enum {
     MOE_ERR_UNSUPPORTED = 2,  /* shape outside the supported set */
     MOE_ERR_WORKSPACE = 3,    /* workspace too small */
     MOE_ERR_CUDA = 4,         /* a CUDA runtime call or launch failed */
-    MOE_ERR_DEVICE = 5,       /* a kernel saw an expert id outside [0, E) */
+    MOE_ERR_DEVICE = 5,       /* a kernel saw an expert id, slot, page or length out of range */
     MOE_ERR_TIMEOUT = 6       /* a kernel's bounded wait gave up */
 } moe_status;
 
@@ -300,6 +300,115 @@ MOE_API int moe_w8a16_workspace_size(int32_t T, int32_t N, int32_t K, int32_t gs
  */
 MOE_API int moe_quantize_int4(const uint16_t *w, int64_t N, int64_t K, int32_t nclip, int32_t *packed,
                       uint16_t *scales, int32_t *choice, void *stream);
+
+/*
+ * The attention block beside the MoE block (no counterpart on the pages, whose
+ * attention kernels stay with the serving engine): per-head norms with the
+ * rotary turn, a paged KV cache in 4 bits, and attention over it.
+ *
+ * Tensors of heads are [T][heads][D] with D contiguous and strides of their
+ * own for tokens and heads (in elements, multiples of 8; the base 16-byte
+ * aligned), so that they may be views of one projection's output.
+ */
+typedef struct {
+    int64_t token, head;
+} moe_strides;
+
+/*
+ * One layer's cache. A row is the D values (64 or 128) of one (token, KV
+ * head): its codes are q + 8 with q in [-8, 7], eight to an int32 word, lowest
+ * nibble first, its scale one bf16, and its values q * scale.
+ *   k_codes, v_codes   int32 [n_pages][Hkv][page_size][D/8]
+ *   k_scales, v_scales bf16  [n_pages][Hkv][page_size]
+ * page_size is a power of two from 16 to 1024; n_pages * page_size < 2^31. The
+ * slot of a token is page * page_size + its place in the page. A scale that is
+ * not finite marks a row that held a value that was not: every query that
+ * sees the row, and no other, gets NaN.
+ */
+typedef struct {
+    int32_t *k_codes;
+    uint16_t *k_scales;
+    int32_t *v_codes;
+    uint16_t *v_scales;
+    int32_t n_pages, Hkv, page_size, D;
+} moe_kv4_cache;
+
+/*
+ * RMS norm of each query and key head, then the rotary turn, in one pass:
+ *   y = x * weight / sqrt(mean(x^2) + eps)            (over the head's D values)
+ *   for the pair i of the first rot values, theta = positions[t] * inv_freq[i]:
+ *     (a, b) -> (a cos theta - b sin theta, a sin theta + b cos theta)
+ * with the pairs (i, i + rot/2), or (2i, 2i + 1) where interleaved is 1. fp32
+ * inside (theta is reduced to a fraction of a turn in integers, so far
+ * positions lose nothing), rounded to bf16 once.
+ *
+ * q, q_out bf16 [T][Hq][D], k, k_out bf16 [T][Hkv][D] (an output may be its
+ * input, with the same strides); q_weight, k_weight bf16 [D] or NULL (ones);
+ * positions int32 [T]; inv_freq f32 [rot/2]. D is 64, 128 or 256; rot a
+ * multiple of 16 from 0 to D (0: norms alone; positions and inv_freq may be
+ * NULL); Hq or Hkv may be 0.
+ */
+MOE_API int moe_qk_norm_rope(const uint16_t *q, moe_strides q_strides, const uint16_t *k, moe_strides k_strides,
+                     const uint16_t *q_weight, const uint16_t *k_weight, const int32_t *positions,
+                     const float *inv_freq, int32_t rot, int32_t interleaved, float eps,
+                     uint16_t *q_out, moe_strides q_out_strides, uint16_t *k_out, moe_strides k_out_strides,
+                     int32_t T, int32_t Hq, int32_t Hkv, int32_t D, void *stream);
+
+/*
+ * Writes token t's rows k[t], v[t] (bf16 [T][Hkv][D]) into the cache at
+ * slots[t] (int32 [T]; -1: not stored), per row:
+ *   s = bf16(max|x| / 7),  q = clamp(rint(x / s), -8, 7)  (fp32 divisions; q = 0 when s = 0)
+ * which is moe_quantize_int4 with nclip = 1 over a row. A row with a NaN or an
+ * infinity gets a NaN scale. Slots must differ. A slot outside [-1, n_pages *
+ * page_size) is left out and sets MOE_ERR_DEVICE in the workspace (at least
+ * 256 bytes, the first 256 zero before its first use).
+ */
+MOE_API int moe_kv4_append(const uint16_t *k, moe_strides k_strides, const uint16_t *v, moe_strides v_strides,
+                   const int32_t *slots, int32_t T, moe_kv4_cache cache, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * The inverse: k[t], v[t] (bf16 [T][Hkv][D], contiguous; outputs) = the values
+ * of the rows at slots[t], rounded to bf16; a slot of -1 reads as zero, one
+ * outside the cache too and sets MOE_ERR_DEVICE.
+ */
+MOE_API int moe_kv4_read(const int32_t *slots, int32_t T, moe_kv4_cache cache, uint16_t *k, uint16_t *v,
+                 void *ws, size_t ws_bytes, void *stream);
+
+/* Workspace bytes moe_kv4_attention needs for these dims (256 serve
+ * moe_kv4_append and moe_kv4_read). */
+MOE_API int moe_kv4_workspace_size(int32_t T, int32_t Hq, int32_t Hkv, int32_t D, size_t *bytes);
+
+/*
+ * Causal attention of B sequences' new tokens over the cache. Sequence b has
+ * the queries [cu_q[b], cu_q[b+1]) of q (cu_q int32 [B+1]; NULL: query b, and
+ * T = B) and lens[b] keys (int32 [B]), the new tokens' own among them; key j
+ * is at page page_table[b][j / page_size] (int32 [B][max_pages]). Of nq
+ * queries, query i sees the first lens[b] - nq + i + 1 keys; query head h
+ * reads KV head h / (Hq / Hkv):
+ *   S_j = scale * q . k_j,  out = sum_j softmax(S)_j v_j,  lse = log sum_j exp(S_j)
+ * A query that sees no key gets out = 0 and lse = -inf.
+ *
+ * q, out bf16 [T][Hq][D] (out must not overlap q or the cache); lse f32
+ * [T][Hq] or NULL. Hq is a multiple of Hkv with at most 32 query heads a KV
+ * head; T <= 2^20, B <= 4096. max_q is the largest number of queries of a
+ * sequence: it decides which kernel runs, never the result.
+ *
+ * Softmax statistics and sums are fp32; a probability is rounded to fp16 where
+ * it feeds the tensor core, the codes enter it exactly, and out is rounded to
+ * bf16 once.
+ *
+ * A page outside [0, n_pages), a length outside [0, max_pages * page_size] and
+ * query offsets that do not rise within [0, T] set MOE_ERR_DEVICE: such a
+ * page's rows read as zero, and the others are brought into their range. Rows
+ * of out that no sequence covers are not written.
+ *
+ * The workspace holds moe_kv4_workspace_size() bytes under the rules of the
+ * MoE calls (all zero before its first use); it may be one that they use.
+ */
+MOE_API int moe_kv4_attention(const uint16_t *q, moe_strides q_strides, moe_kv4_cache cache,
+                      const int32_t *page_table, int32_t max_pages, const int32_t *lens, const int32_t *cu_q,
+                      int32_t B, int32_t T, int32_t Hq, int32_t max_q, float scale,
+                      uint16_t *out, moe_strides out_strides, float *lse, void *ws, size_t ws_bytes, void *stream);
 
 /*
  * Which kernels a forward call of dims `d` runs (a host-only query, no

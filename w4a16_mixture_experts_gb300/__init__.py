@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -24,7 +25,8 @@ __all__ = [
     "MoeError", "moe_dims", "lib", "build", "moe_status_str", "moe_version", "moe_workspace_size",
     "workspace", "moe_route", "moe_route_shared", "shared_workspace", "moe_w4a16_forward", "moe_w4a16_forward_rms", "moe_permute",
     "moe_pack_int4", "moe_quantize_int4", "moe_w8a16_linear", "moe_w8a16_workspace_size", "moe_check_device_error", "moe_profile_events", "moe_w4a16_forward_noalloc",
-    "moe_noalloc_check_device_error", "moe_forward_plan", "STATUS",
+    "moe_noalloc_check_device_error", "moe_forward_plan", "STATUS", "Kv4Cache", "kv4_cache", "kv4_workspace",
+    "moe_kv4_workspace_size", "moe_qk_norm_rope", "moe_kv4_append", "moe_kv4_read", "moe_kv4_attention",
 ]
 
 _DIR = os.path.dirname(os.path.abspath(__file__))
@@ -46,6 +48,16 @@ class moe_dims(ctypes.Structure):
 
     def __repr__(self):
         return "moe_dims(T=%d, H=%d, E=%d, k=%d, I=%d)" % (self.T, self.H, self.E, self.k, self.I)
+
+
+class moe_strides(ctypes.Structure):
+    _fields_ = [("token", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class moe_kv4_cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("D", ctypes.c_int32)]
 
 
 _lib = None
@@ -92,6 +104,15 @@ def lib() -> ctypes.CDLL:
         L.moe_noalloc_check_device_error.argtypes, L.moe_noalloc_check_device_error.restype = [P], I
         L.moe_profile_events.argtypes, L.moe_profile_events.restype = [P, P], I
         L.moe_forward_plan.argtypes, L.moe_forward_plan.restype = [D, ctypes.POINTER(ctypes.c_int32)], I
+        S, C, I32, F = moe_strides, moe_kv4_cache, ctypes.c_int32, ctypes.c_float
+        L.moe_qk_norm_rope.argtypes = [P, S, P, S, P, P, P, P, I32, I32, F, P, S, P, S, I32, I32, I32, I32, P]
+        L.moe_qk_norm_rope.restype = I
+        L.moe_kv4_append.argtypes, L.moe_kv4_append.restype = [P, S, P, S, P, I32, C, P, Z, P], I
+        L.moe_kv4_read.argtypes, L.moe_kv4_read.restype = [P, I32, C, P, P, P, Z, P], I
+        L.moe_kv4_workspace_size.argtypes = [I32, I32, I32, I32, ctypes.POINTER(Z)]
+        L.moe_kv4_workspace_size.restype = I
+        L.moe_kv4_attention.argtypes = [P, S, C, P, I32, P, P, I32, I32, I32, I32, F, P, S, P, P, Z, P]
+        L.moe_kv4_attention.restype = I
         _lib = L
     return _lib
 
@@ -378,6 +399,181 @@ def moe_w8a16_workspace_size(T: int, N: int, K: int, gs: int) -> int:
     n = ctypes.c_size_t(0)
     _check(lib().moe_w8a16_workspace_size(T, N, K, gs, ctypes.byref(n)), "moe_w8a16_workspace_size")
     return n.value
+
+
+class Kv4Cache(NamedTuple):
+    """One layer's paged 4-bit KV cache: codes int32 [pages, Hkv, page_size, D/8] (q + 8, eight to a
+    word, lowest nibble first) and scales bf16 [pages, Hkv, page_size], of K and of V. The slot of a
+    token is page * page_size + its place in the page."""
+    k_codes: torch.Tensor
+    k_scales: torch.Tensor
+    v_codes: torch.Tensor
+    v_scales: torch.Tensor
+
+
+def kv4_cache(n_pages: int, Hkv: int, page_size: int, D: int, device=None) -> Kv4Cache:
+    """A cache of zeroed rows (D 64 or 128; page_size a power of two from 16 to 1024)."""
+    device = device if device is not None else "cuda"
+    codes = [torch.full((n_pages, Hkv, page_size, D // 8), -0x77777778, dtype=torch.int32, device=device)
+             for _ in range(2)]
+    scales = [torch.zeros(n_pages, Hkv, page_size, dtype=torch.bfloat16, device=device) for _ in range(2)]
+    return Kv4Cache(codes[0], scales[0], codes[1], scales[1])
+
+
+def moe_kv4_workspace_size(T: int, Hq: int, Hkv: int, D: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_kv4_workspace_size(T, Hq, Hkv, D, ctypes.byref(n)), "moe_kv4_workspace_size")
+    return n.value
+
+
+def kv4_workspace(T: int = 0, Hq: int = 1, Hkv: int = 1, D: int = 128, device=None) -> torch.Tensor:
+    """A zeroed uint8 workspace of moe_kv4_workspace_size bytes (with no dims: what
+    moe_kv4_append and moe_kv4_read need)."""
+    n = moe_kv4_workspace_size(T, Hq, Hkv, D) if T else 256
+    return torch.zeros(n, dtype=torch.uint8, device=device if device is not None else "cuda")
+
+
+def _heads(t, name, T=None, D=None):
+    """The strides of a bf16 [T, heads, D] CUDA tensor with contiguous D."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    shape = t.shape
+    if t.dtype != torch.bfloat16 or len(shape) != 3 or (T is not None and shape[0] != T) or (
+            D is not None and shape[2] != D):
+        raise ValueError("%s must be bf16 [%s, heads, %s], got %s %s" % (
+            name, "T" if T is None else T, "D" if D is None else D, t.dtype, tuple(shape)))
+    st = t.stride()
+    if not t.is_cuda or (st[2] != 1 and shape[2] > 1):
+        raise ValueError("%s must be a CUDA tensor with contiguous head values" % name)
+    # (a dimension of one entry has no stride that matters)
+    return moe_strides(st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0)
+
+
+def _vec(t, name, dtype, n=None):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype != dtype or t.dim() != 1 or (n is not None and t.shape[0] != n) or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s CUDA tensor%s, got %s %s"
+                         % (name, dtype, "" if n is None else " of %d values" % n, t.dtype, tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _cache(c) -> moe_kv4_cache:
+    kc, ks, vc, vs = c
+    _need(kc, "k_codes", torch.int32, 4)
+    _need(ks, "k_scales", torch.bfloat16, 3)
+    _need(vc, "v_codes", torch.int32, 4)
+    _need(vs, "v_scales", torch.bfloat16, 3)
+    n, h, p, w = kc.shape
+    if vc.shape != kc.shape or ks.shape != (n, h, p) or vs.shape != (n, h, p):
+        raise ValueError("a cache holds codes [pages, Hkv, page_size, D/8] and scales [pages, Hkv, page_size], got %s %s %s %s"
+                         % tuple(tuple(t.shape) for t in c))
+    return moe_kv4_cache(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), n, h, p, w * 8)
+
+
+def moe_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6,
+                     interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """RMS norm of each head of q [T, Hq, D] and k [T, Hkv, D], then the rotary turn of the first
+    2 * len(inv_freq) values by positions[t] * inv_freq[i], in one pass.
+
+    q and k are bf16 and may be views (their D values contiguous); the outputs may be the inputs.
+    positions int32 [T], inv_freq f32 [rot/2] (both None: norms alone), weights bf16 [D] or None.
+    The pairs are (i, i + rot/2), or (2i, 2i + 1) with interleaved. Returns (q_out, k_out).
+    """
+    qs = _heads(q, "q")
+    T, Hq, D = q.shape
+    ks = _heads(k, "k", T, D)
+    if q_out is None:
+        q_out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(T, k.shape[1], D, dtype=torch.bfloat16, device=q.device)
+    qos, kos = _heads(q_out, "q_out", T, D), _heads(k_out, "k_out", T, D)
+    if q_out.shape[1] != Hq or k_out.shape[1] != k.shape[1]:
+        raise ValueError("q_out and k_out must have the heads of q and k")
+    pos = fr = None
+    rot = 0
+    if inv_freq is not None:
+        fr, rot = _vec(inv_freq, "inv_freq", torch.float32), 2 * inv_freq.shape[0]
+        pos = _vec(positions, "positions", torch.int32, T)
+    _check(lib().moe_qk_norm_rope(q.data_ptr(), qs, k.data_ptr(), ks,
+                                  None if q_weight is None else _vec(q_weight, "q_weight", torch.bfloat16, D),
+                                  None if k_weight is None else _vec(k_weight, "k_weight", torch.bfloat16, D),
+                                  pos, fr, rot, 1 if interleaved else 0, eps, q_out.data_ptr(), qos, k_out.data_ptr(),
+                                  kos, T, Hq, k.shape[1], D, _stream(stream)), "moe_qk_norm_rope")
+    return q_out, k_out
+
+
+def moe_kv4_append(k, v, slots, cache: Kv4Cache, ws=None, stream=None):
+    """Quantises token t's rows k[t], v[t] (bf16 [T, Hkv, D], views allowed) into the cache at
+    slots[t] (int32 [T]; -1: not stored). ws: kv4_workspace(), whose error word
+    moe_check_device_error reads. Returns the cache."""
+    c = _cache(cache)
+    ks = _heads(k, "k", None, c.D)
+    T = k.shape[0]
+    vs = _heads(v, "v", T, c.D)
+    if k.shape[1] != c.Hkv or v.shape[1] != c.Hkv:
+        raise ValueError("k and v must have the cache's %d heads, got %d and %d" % (c.Hkv, k.shape[1], v.shape[1]))
+    if ws is None:
+        ws = kv4_workspace(device=k.device)
+    _check(lib().moe_kv4_append(k.data_ptr(), ks, v.data_ptr(), vs, _vec(slots, "slots", torch.int32, T), T, c,
+                                ws.data_ptr(), ws.numel(), _stream(stream)), "moe_kv4_append")
+    return cache
+
+
+def moe_kv4_read(slots, cache: Kv4Cache, k_out=None, v_out=None, ws=None, stream=None):
+    """The cache's rows at slots (int32 [T]; -1 reads as zero) as bf16 values: (k, v) [T, Hkv, D]."""
+    c = _cache(cache)
+    at = _vec(slots, "slots", torch.int32)
+    shape = (slots.shape[0], c.Hkv, c.D)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        _need(t, name, torch.bfloat16, 3)
+        if t.shape != shape:
+            raise ValueError("%s must be %s, got %s" % (name, shape, tuple(t.shape)))
+    if ws is None:
+        ws = kv4_workspace(device=slots.device)
+    _check(lib().moe_kv4_read(at, shape[0], c, k_out.data_ptr(), v_out.data_ptr(), ws.data_ptr(), ws.numel(),
+                              _stream(stream)), "moe_kv4_read")
+    return k_out, v_out
+
+
+def moe_kv4_attention(q, cache: Kv4Cache, page_table, lens, cu_q=None, max_q: int = 1, scale=None, out=None,
+                      lse=None, ws=None, stream=None):
+    """Causal attention of q [T, Hq, D] (bf16, views allowed) over the 4-bit cache.
+
+    Sequence b has the queries [cu_q[b], cu_q[b+1]) (cu_q int32 [B+1]; None: one each) and lens[b] keys
+    (int32 [B]), the new tokens' own among them, in the pages page_table[b] (int32 [B, max_pages]).
+    max_q is the largest number of queries of a sequence. scale defaults to D ** -0.5.
+    ws: kv4_workspace(T, Hq, Hkv, D). Returns out, or (out, lse f32 [T, Hq]) where lse is given
+    (a tensor, or True to have it made)."""
+    c = _cache(cache)
+    qs = _heads(q, "q", None, c.D)
+    T, Hq, D = q.shape
+    B = lens.shape[0]
+    at = _vec(lens, "lens", torch.int32)
+    cu = None if cu_q is None else _vec(cu_q, "cu_q", torch.int32, B + 1)
+    _need(page_table, "page_table", torch.int32, 2)
+    if page_table.shape[0] != B:
+        raise ValueError("page_table must have a row for each of the %d sequences, got %s" % (B, tuple(page_table.shape)))
+    if out is None:
+        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device)
+    os_ = _heads(out, "out", T, D)
+    if lse is True:
+        lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, 2)
+    if out.shape[1] != Hq or (lse is not None and lse.shape != (T, Hq)):
+        raise ValueError("out must be [T, Hq, D] and lse [T, Hq]")
+    if ws is None:
+        ws = kv4_workspace(T, Hq, c.Hkv, D, device=q.device)
+    _check(lib().moe_kv4_attention(q.data_ptr(), qs, c, page_table.data_ptr(), page_table.shape[1], at, cu, B, T, Hq,
+                                   max_q, D ** -0.5 if scale is None else scale, out.data_ptr(), os_,
+                                   None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
+                                   _stream(stream)), "moe_kv4_attention")
+    return out if lse is None else (out, lse)
 
 
 def moe_profile_events(before=None, after=None):

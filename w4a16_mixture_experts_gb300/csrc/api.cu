@@ -1,6 +1,7 @@
 // C-ABI entry points of libw4a16moe: argument checks, workspace layout and
 // kernel sequencing. No allocation, no synchronisation (except in
 // moe_check_device_error, which exists to synchronise).
+#include <math.h>
 #include <stdint.h>
 
 #include <mutex>
@@ -143,7 +144,7 @@ const char *moe_status_str(int status) {
         case MOE_ERR_UNSUPPORTED: return "unsupported shape";
         case MOE_ERR_WORKSPACE: return "workspace too small";
         case MOE_ERR_CUDA: return "CUDA runtime or launch error";
-        case MOE_ERR_DEVICE: return "a kernel saw an expert id outside [0, E)";
+        case MOE_ERR_DEVICE: return "a kernel saw an expert id, slot, page or length out of range";
         case MOE_ERR_TIMEOUT: return "a kernel's bounded wait gave up";
         default: return "unknown status";
     }
@@ -323,6 +324,127 @@ int moe_w8a16_workspace_size(int32_t T, int32_t N, int32_t K, int32_t gs, size_t
     }
     *bytes = n;
     return MOE_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// [T][heads][D] with D contiguous: 16-byte aligned rows.
+bool rows_ok(const void *p, const moe_strides &s, bool empty) {
+    return ptr_ok(p, empty) && s.token >= 0 && s.head >= 0 && s.token % 8 == 0 && s.head % 8 == 0;
+}
+
+// An output's rows must not overlap one another either.
+bool out_rows_ok(const void *p, const moe_strides &s, int T, int heads, int D) {
+    const bool empty = T == 0 || heads == 0;
+    if (!rows_ok(p, s, empty)) return false;
+    if (empty || (T == 1 && heads == 1)) return true;
+    if (T == 1) return s.head >= D;
+    if (heads == 1) return s.token >= D;
+    if (s.token >= s.head) return s.head >= D && s.token >= (heads - 1) * s.head + D;
+    return s.token >= D && s.head >= (T - 1) * s.token + D;
+}
+
+int check_cache(const moe_kv4_cache &c) {
+    if (c.n_pages <= 0 || c.Hkv <= 0 || c.page_size <= 0 || c.D <= 0) return MOE_ERR_INVALID_ARG;
+    if (c.D != 64 && c.D != 128) return MOE_ERR_UNSUPPORTED;
+    if (c.page_size < 16 || c.page_size > 1024 || (c.page_size & (c.page_size - 1))) return MOE_ERR_UNSUPPORTED;
+    if ((int64_t)c.n_pages * c.page_size >= ((int64_t)1 << 31) || c.Hkv > 1024) return MOE_ERR_UNSUPPORTED;
+    if (!ptr_ok(c.k_codes, false) || !ptr_ok(c.k_scales, false) || !ptr_ok(c.v_codes, false) ||
+        !ptr_ok(c.v_scales, false))
+        return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+int check_rows_ws(const void *ws, size_t ws_bytes) {
+    if (!ws || !aligned16(ws)) return MOE_ERR_INVALID_ARG;
+    return ws_bytes < sizeof(Ctrl) ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
+bool aligned4(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+
+extern "C" {
+
+int moe_qk_norm_rope(const uint16_t *q, moe_strides q_strides, const uint16_t *k, moe_strides k_strides,
+                     const uint16_t *q_weight, const uint16_t *k_weight, const int32_t *positions,
+                     const float *inv_freq, int32_t rot, int32_t interleaved, float eps, uint16_t *q_out,
+                     moe_strides q_out_strides, uint16_t *k_out, moe_strides k_out_strides, int32_t T, int32_t Hq,
+                     int32_t Hkv, int32_t D, void *stream) {
+    if (T < 0 || Hq < 0 || Hkv < 0 || D <= 0 || rot < 0 || rot > D || (interleaved != 0 && interleaved != 1) ||
+        !(eps >= 0.f))
+        return MOE_ERR_INVALID_ARG;
+    if ((D != 64 && D != 128 && D != 256) || rot % 16) return MOE_ERR_UNSUPPORTED;
+    if (T > (1 << 20) || Hq > 1024 || Hkv > 1024) return MOE_ERR_UNSUPPORTED;
+    const bool no_q = T == 0 || Hq == 0, no_k = T == 0 || Hkv == 0;
+    if (!rows_ok(q, q_strides, no_q) || !rows_ok(k, k_strides, no_k) ||
+        !out_rows_ok(q_out, q_out_strides, T, Hq, D) || !out_rows_ok(k_out, k_out_strides, T, Hkv, D))
+        return MOE_ERR_INVALID_ARG;
+    if ((q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight))) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && rot > 0 && (!aligned4(positions) || !aligned4(inv_freq))) return MOE_ERR_INVALID_ARG;
+    if (no_q && no_k) return MOE_OK;
+    return cuda_status(launch_norm_rope(q, q_strides, k, k_strides, q_weight, k_weight, positions, inv_freq, rot,
+                                        interleaved != 0, eps, q_out, q_out_strides, k_out, k_out_strides, T, Hq, Hkv,
+                                        D, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_kv4_append(const uint16_t *k, moe_strides k_strides, const uint16_t *v, moe_strides v_strides,
+                   const int32_t *slots, int32_t T, moe_kv4_cache cache, void *ws, size_t ws_bytes, void *stream) {
+    if (T < 0) return MOE_ERR_INVALID_ARG;
+    int rc = check_cache(cache);
+    if (rc) return rc;
+    if (T > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+    if (!rows_ok(k, k_strides, T == 0) || !rows_ok(v, v_strides, T == 0) || (T > 0 && !aligned4(slots)))
+        return MOE_ERR_INVALID_ARG;
+    if ((rc = check_rows_ws(ws, ws_bytes))) return rc;
+    if (T == 0) return MOE_OK;
+    return cuda_status(launch_kv4_append(k, k_strides, v, v_strides, slots, T, cache, reinterpret_cast<Ctrl *>(ws),
+                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_kv4_read(const int32_t *slots, int32_t T, moe_kv4_cache cache, uint16_t *k, uint16_t *v, void *ws,
+                 size_t ws_bytes, void *stream) {
+    if (T < 0) return MOE_ERR_INVALID_ARG;
+    int rc = check_cache(cache);
+    if (rc) return rc;
+    if (T > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+    if (!ptr_ok(k, T == 0) || !ptr_ok(v, T == 0) || (T > 0 && !aligned4(slots))) return MOE_ERR_INVALID_ARG;
+    if ((rc = check_rows_ws(ws, ws_bytes))) return rc;
+    if (T == 0) return MOE_OK;
+    return cuda_status(launch_kv4_read(slots, T, cache, k, v, reinterpret_cast<Ctrl *>(ws),
+                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_kv4_workspace_size(int32_t T, int32_t Hq, int32_t Hkv, int32_t D, size_t *bytes) {
+    if (!bytes || T < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv) return MOE_ERR_INVALID_ARG;
+    if ((D != 64 && D != 128) || Hq / Hkv > 32 || T > (1 << 20) || Hkv > 1024) return MOE_ERR_UNSUPPORTED;
+    *bytes = kv4_workspace_bytes(T, Hq, Hkv, D);
+    return MOE_OK;
+}
+
+int moe_kv4_attention(const uint16_t *q, moe_strides q_strides, moe_kv4_cache cache, const int32_t *page_table,
+                      int32_t max_pages, const int32_t *lens, const int32_t *cu_q, int32_t B, int32_t T, int32_t Hq,
+                      int32_t max_q, float scale, uint16_t *out, moe_strides out_strides, float *lse, void *ws,
+                      size_t ws_bytes, void *stream) {
+    int rc = check_cache(cache);
+    if (rc) return rc;
+    size_t need = 0;
+    if ((rc = moe_kv4_workspace_size(T, Hq, cache.Hkv, cache.D, &need))) return rc;
+    if (B < 0 || max_pages < 0 || max_q < 0 || (!cu_q && T != B) || (T > 0 && B == 0) || !(fabsf(scale) <= 3.4e38f))
+        return MOE_ERR_INVALID_ARG;
+    if (B > 4096 || (int64_t)max_pages * cache.page_size >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+    if (!rows_ok(q, q_strides, T == 0) || !out_rows_ok(out, out_strides, T, Hq, cache.D)) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!aligned4(lens) || (cu_q && !aligned4(cu_q)) || (max_pages > 0 && !aligned4(page_table)) ||
+                  (lse && !aligned4(lse))))
+        return MOE_ERR_INVALID_ARG;
+    if (!ws || !aligned16(ws)) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+    if (T == 0) return MOE_OK;
+    return cuda_status(launch_kv4_attention(q, q_strides, cache, page_table, max_pages, lens, cu_q, B, T, Hq, max_q,
+                                            scale, out, out_strides, lse, ws,
+                                            reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int moe_profile_events(void *before_experts, void *after_experts) {
