@@ -3,23 +3,15 @@
 // Query i of a sequence with nq queries and len keys sits at position
 // len - nq + i and sees the keys up to it: out = sum_j softmax(scale q.k_j) v_j,
 // lse = log sum_j exp(scale q.k_j); without a key out = 0 and lse = -inf.
-#include "kv4.cuh"
+#include "kv4_attention.cuh"
 
 namespace moe {
 
+cudaError_t launch_kv4_decode(const kv4::Attn &p, int rows, cudaStream_t s);
+
 namespace {
 
-struct Attn {
-    kv4::Batch b;
-    const uint16_t *q;
-    moe_strides qs, os;
-    moe_kv4_cache c;
-    uint16_t *out;
-    float *lse;
-    Ctrl *ctrl;
-    float scale;
-    int Hq, G;
-};
+using kv4::Attn;
 
 // One CTA of 128 threads a row (query, head): a thread scores one key of each
 // 128, then adds up one value column.
@@ -112,18 +104,23 @@ __global__ void __launch_bounds__(128) attention_rows_kernel(Attn p) {
 
 }  // namespace
 
+// The rows that share one pass over their keys decide: up to 32 of a sequence
+// go to the streaming kernel.
+constexpr int kDecodeRows = 32;
+
 size_t kv4_workspace_bytes(int T, int Hq, int Hkv, int D) {
-    (void)T, (void)Hq, (void)Hkv, (void)D;
-    return sizeof(Ctrl);
+    (void)T, (void)Hq, (void)Hkv;
+    return align_up(kv4::kPartOff + sizeof(float) * 2 * kv4::kMaxCtas * kv4::part_floats(kDecodeRows, D), 256);
 }
 
 cudaError_t launch_kv4_attention(const uint16_t *q, moe_strides qs, const moe_kv4_cache &c, const int32_t *table,
                                  int max_pages, const int32_t *lens, const int32_t *cu_q, int B, int T, int Hq,
                                  int max_q, float scale, uint16_t *out, moe_strides os, float *lse, void *ws,
                                  cudaStream_t s) {
-    (void)max_q;
+    const int G = Hq / c.Hkv;
     Attn p{{table, lens, cu_q, B, T, max_pages, __builtin_ctz((unsigned)c.page_size)}, q, qs, os, c, out, lse,
-           reinterpret_cast<Ctrl *>(ws), scale, Hq, Hq / c.Hkv};
+           reinterpret_cast<Ctrl *>(ws), ws_at<uint32_t>(ws, kv4::kTicketOff), ws_at<float>(ws, kv4::kPartOff), scale, Hq, G};
+    if ((long long)max_q * G <= kDecodeRows) return launch_kv4_decode(p, max_q * G, s);
     const dim3 grid(T, Hq);
     return c.D == 64 ? launch_pdl(attention_rows_kernel<64>, grid, 128, 0, s, p)
                      : launch_pdl(attention_rows_kernel<128>, grid, 128, 0, s, p);

@@ -1,0 +1,217 @@
+// What the attention kernels over the 4-bit cache share: their arguments, how
+// the work is dealt to the CTAs, and how an item's parts are joined.
+//
+// An item is up to R query rows of one (sequence, KV head); row r of a sequence
+// is query r / G, head r % G of the group. Its work is a number of units, each a
+// fixed count of keys. All items' units lie one after another and CTA c of C
+// takes the units [U c / C, U (c + 1) / C), whatever items they belong to: an
+// even share for any mix of lengths. An item that lies in several CTAs' shares
+// is joined by the last of them to finish, in the CTAs' order, so that the
+// result does not depend on which that is.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "kv4.cuh"
+
+namespace moe {
+namespace kv4 {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNoMax = -3e38f;   // below every score: nothing seen yet
+
+// Partial results of at most this many CTAs; a fixed figure, so that the
+// workspace's size does not depend on the device (152 SMs, two CTAs each).
+constexpr int kMaxCtas = 320;
+// The tickets lie in the workspace's first region that calls leave at zero.
+constexpr size_t kTicketOff = 512, kPartOff = 512 + (size_t)kMaxE * kCtrStride * 4;
+static_assert((size_t)kMaxCtas * 4 <= kPartOff - kTicketOff, "tickets");
+
+struct Attn {
+    Batch b;
+    const uint16_t *q;
+    moe_strides qs, os;
+    moe_kv4_cache c;
+    uint16_t *out;
+    float *lse;
+    Ctrl *ctrl;
+    uint32_t *ticket;   // [kMaxCtas]
+    float *part;        // [kMaxCtas][2] x part_floats(R, D)
+    float scale;
+    int Hq, G;
+};
+
+// A part of an item: the running maximum and sum of each row, the exponent of
+// its values, and the rows' values.
+__host__ __device__ constexpr int part_floats(int R, int D) { return 2 * R + 4 + R * D; }
+
+__device__ inline float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 2^(e - 127) for a biased exponent e in [1, 254].
+__device__ inline float pow2_biased(int e) { return __uint_as_float((uint32_t)e << 23); }
+
+// The biased exponent that brings a row with the largest magnitude `bits`
+// (bf16) to [1, 2) (or near it at the ends of the range): the row is
+// multiplied by 2^(127 - e).
+__device__ inline int norm_exponent(uint32_t bits) {
+    const int e = (int)(bits >> 7) & 0xFF;
+    return e == 0xFF ? 127 : min(max(e, 1), 253);
+}
+
+// Nibble pairs of a word as fp16x2, exactly. OR-ing a nibble into the mantissa
+// of 1024 (bits 0-3) or of 64 (bits 4-7) gives 1024 + n or 64 + n, so two of
+// the word's four pairs need no shift.
+__device__ inline uint32_t nib_lo(uint32_t w) {   // bits 0-3 of each half, less 8
+    uint32_t v;
+    asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(v) : "r"(w), "r"(0x64006400u));
+    const __half2 r = __hsub2(*reinterpret_cast<__half2 *>(&v), __float2half2_rn(1032.f));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ inline uint32_t nib_hi(uint32_t w) {   // bits 4-7
+    uint32_t v;
+    asm("lop3.b32 %0, %1, 0x00F000F0, %2, 0xEA;" : "=r"(v) : "r"(w), "r"(0x54005400u));
+    const __half2 r = __hsub2(*reinterpret_cast<__half2 *>(&v), __float2half2_rn(72.f));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// Keys that the last row of row tile qt sees (all rows' keys are a prefix of them).
+__device__ inline int tile_keys(const Seq &s, int G, int R, int qt) {
+    const int last = (min((qt + 1) * R, s.nq * G) - 1) / G;
+    return min(max(s.len - s.nq + last + 1, 0), s.len);
+}
+
+// Units of a sequence's row tile: at least one, so that rows that see no key
+// are written too.
+template <int kKeys>
+__device__ inline int tile_units(const Seq &s, int G, int R, int qt) {
+    return max(1, (tile_keys(s, G, R, qt) + kKeys - 1) / kKeys);
+}
+
+// pre[b] = units of the sequences before b, for all of them: every CTA forms
+// it, a thread a sequence. Returns the total.
+template <int kThreads, int kKeys>
+__device__ long long scan_units(const Attn &p, int R, long long *pre, long long *warp_sums) {
+    long long base = 0;
+    for (int b0 = 0; b0 < p.b.B; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        long long n = 0;
+        if (b < p.b.B) {
+            const Seq s = seq_of(p.b, b, p.ctrl);
+            const int tiles = (s.nq * p.G + R - 1) / R;
+            for (int qt = 0; qt < tiles; ++qt) n += tile_units<kKeys>(s, p.G, R, qt);
+            n *= p.c.Hkv;
+        }
+        long long inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+            if ((threadIdx.x & 31) >= o) inc += v;
+        }
+        if ((threadIdx.x & 31) == 31) warp_sums[threadIdx.x >> 5] = inc;
+        __syncthreads();
+        long long before = base;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < (int)(threadIdx.x >> 5)) before += warp_sums[w];
+            base += warp_sums[w];
+        }
+        if (b < p.b.B) pre[b] = before + inc - n;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) pre[p.b.B] = base;
+    __syncthreads();
+    return base;
+}
+
+struct Item {
+    int b, h, qt;
+    int units;            // of the item
+    long long first;      // its first unit
+    Seq s;
+};
+
+// The item that holds unit u (u below the total).
+template <int kKeys>
+__device__ Item find_item(const Attn &p, int R, const long long *pre, long long u) {
+    Item it;
+    int lo = 0;
+    for (int hi = p.b.B; hi - lo > 1;) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid] <= u) lo = mid;
+        else hi = mid;
+    }
+    it.b = lo;   // (sequences without units share their successor's pre: the last of them is the one)
+    it.s = seq_of(p.b, lo, p.ctrl);
+    const long long per_head = (pre[lo + 1] - pre[lo]) / p.c.Hkv;
+    it.h = (int)((u - pre[lo]) / per_head);
+    long long at = pre[lo] + it.h * per_head;
+    it.qt = 0;
+    for (;;) {
+        it.units = tile_units<kKeys>(it.s, p.G, R, it.qt);
+        if (u < at + it.units) break;
+        at += it.units;
+        ++it.qt;
+    }
+    it.first = at;
+    return it;
+}
+
+__device__ inline uint32_t bf16x2_of(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Four finished values of row r of an item (and the row's log-sum-exp): value
+// times 2^(F - 127) over the row's sum; a row without a key is zero.
+__device__ inline void write_row4(const Attn &p, const Item &it, int R, int r, int d, float4 v, float m, float l, int F) {
+    const int rr = it.qt * R + r, i = rr / p.G, head = it.h * p.G + rr - i * p.G;
+    const size_t tok = (size_t)(it.s.q0 + i);
+    const float inv = l == 0.f ? 0.f : 1.f / l, up = pow2_biased(F);
+    *reinterpret_cast<uint2 *>(p.out + tok * p.os.token + (size_t)head * p.os.head + d) =
+        make_uint2(bf16x2_of(v.x * inv * up, v.y * inv * up), bf16x2_of(v.z * inv * up, v.w * inv * up));
+    if (d == 0 && p.lse) p.lse[tok * p.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// Joins the parts of an item that CTAs c0 .. c1 left, in their order: the
+// first is its CTA's last part, the others are their CTAs' first.
+template <int kThreads, int R, int D>
+__device__ void join_parts(const Attn &p, const Item &it, int rows, int c0, int c1) {
+    constexpr int N = part_floats(R, D);
+    auto at = [&](int c) { return p.part + (size_t)(c * 2 + (c == c0)) * N; };
+    for (int x = threadIdx.x; x < rows * (D / 4); x += kThreads) {
+        const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+        float M = kNoMax, L = 0.f;
+        int F = 1;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int c = c0; c <= c1; ++c) {
+            const float *q = at(c);
+            const float m = __ldcg(q + r), l = __ldcg(q + R + r);
+            const int f = __float_as_int(__ldcg(q + 2 * R));
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(q + 2 * R + 4 + r * D + d));
+            const float Mn = fmaxf(M, m);
+            const int Fn = max(F, f);
+            const float a = exp2_approx(M - Mn), b = exp2_approx(m - Mn);
+            const float av = Fn - F > 126 ? 0.f : a * pow2_biased(127 + F - Fn);
+            const float bv = Fn - f > 126 ? 0.f : b * pow2_biased(127 + f - Fn);
+            L = L * a + l * b;
+            acc.x = acc.x * av + v.x * bv;
+            acc.y = acc.y * av + v.y * bv;
+            acc.z = acc.z * av + v.z * bv;
+            acc.w = acc.w * av + v.w * bv;
+            M = Mn;
+            F = Fn;
+        }
+        write_row4(p, it, R, r, d, acc, M, L, F);
+    }
+}
+
+// The CTA whose share holds unit u.
+__device__ inline int cta_of(long long u, long long U, int C) { return (int)(((u + 1) * C - 1) / U); }
+
+}  // namespace kv4
+}  // namespace moe
