@@ -21,9 +21,15 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -3e38f;   // below every score: nothing seen yet
 
-// Partial results of at most this many CTAs; a fixed figure, so that the
-// workspace's size does not depend on the device (152 SMs, two CTAs each).
-constexpr int kMaxCtas = 320;
+// Up to so many rows of a sequence share one streaming pass; more go to the
+// tensor core.
+constexpr int kDecodeRows = 32;
+constexpr int kPromptRows = 256;
+
+// Partial results of at most so many CTAs; fixed figures, so that the
+// workspace's size does not depend on the device (152 SMs; the streaming kernel
+// runs two CTAs on each).
+constexpr int kMaxCtas = 320, kMaxPromptCtas = 160;
 // The tickets lie in the workspace's first region that calls leave at zero.
 constexpr size_t kTicketOff = 512, kPartOff = 512 + (size_t)kMaxE * kCtrStride * 4;
 static_assert((size_t)kMaxCtas * 4 <= kPartOff - kTicketOff, "tickets");
@@ -37,7 +43,7 @@ struct Attn {
     float *lse;
     Ctrl *ctrl;
     uint32_t *ticket;   // [kMaxCtas]
-    float *part;        // [kMaxCtas][2] x part_floats(R, D)
+    float *part;        // [CTAs][2] x part_floats(R, D)
     float scale;
     int Hq, G;
 };
@@ -93,19 +99,30 @@ __device__ inline int tile_units(const Seq &s, int G, int R, int qt) {
 }
 
 // pre[b] = units of the sequences before b, for all of them: every CTA forms
-// it, a thread a sequence. Returns the total.
+// it, a thread a sequence (a warp, for a sequence of many row tiles). Returns
+// the total.
 template <int kThreads, int kKeys>
 __device__ long long scan_units(const Attn &p, int R, long long *pre, long long *warp_sums) {
     long long base = 0;
     for (int b0 = 0; b0 < p.b.B; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
         long long n = 0;
-        if (b < p.b.B) {
-            const Seq s = seq_of(p.b, b, p.ctrl);
-            const int tiles = (s.nq * p.G + R - 1) / R;
+        Seq s{0, 0, 0};
+        if (b < p.b.B) s = seq_of(p.b, b, p.ctrl);
+        const int tiles = (s.nq * p.G + R - 1) / R;
+        if (tiles <= 2)
             for (int qt = 0; qt < tiles; ++qt) n += tile_units<kKeys>(s, p.G, R, qt);
-            n *= p.c.Hkv;
+        for (uint32_t many = __ballot_sync(0xffffffffu, tiles > 2); many; many &= many - 1) {
+            const int src = __ffs(many) - 1;
+            const Seq o{0, __shfl_sync(0xffffffffu, s.nq, src), __shfl_sync(0xffffffffu, s.len, src)};
+            const int ot = (o.nq * p.G + R - 1) / R;
+            long long m = 0;
+            for (int qt = threadIdx.x & 31; qt < ot; qt += 32) m += tile_units<kKeys>(o, p.G, R, qt);
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) m += __shfl_xor_sync(0xffffffffu, m, x);
+            if ((threadIdx.x & 31) == src) n = m;
         }
+        n *= p.c.Hkv;
         long long inc = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -134,7 +151,7 @@ struct Item {
     Seq s;
 };
 
-// The item that holds unit u (u below the total).
+// The item that holds unit u (u below the total); a whole warp calls it.
 template <int kKeys>
 __device__ Item find_item(const Attn &p, int R, const long long *pre, long long u) {
     Item it;
@@ -149,15 +166,42 @@ __device__ Item find_item(const Attn &p, int R, const long long *pre, long long 
     const long long per_head = (pre[lo + 1] - pre[lo]) / p.c.Hkv;
     it.h = (int)((u - pre[lo]) / per_head);
     long long at = pre[lo] + it.h * per_head;
-    it.qt = 0;
-    for (;;) {
-        it.units = tile_units<kKeys>(it.s, p.G, R, it.qt);
-        if (u < at + it.units) break;
-        at += it.units;
-        ++it.qt;
+    const int tiles = (it.s.nq * p.G + R - 1) / R, lane = threadIdx.x & 31;
+    for (int q0 = 0;; q0 += 32) {   // 32 row tiles at a time
+        const int n = q0 + lane < tiles ? tile_units<kKeys>(it.s, p.G, R, q0 + lane) : 0;
+        int inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        const uint32_t here = __ballot_sync(0xffffffffu, u < at + inc);
+        if (here || q0 + 32 >= tiles) {
+            const int src = here ? __ffs(here) - 1 : 0;
+            it.qt = q0 + src;
+            it.units = __shfl_sync(0xffffffffu, n, src);
+            it.first = at + __shfl_sync(0xffffffffu, inc - n, src);
+            return it;
+        }
+        at += __shfl_sync(0xffffffffu, inc, 31);
     }
-    it.first = at;
-    return it;
+}
+
+// The item after `it`, where there is one.
+template <int kKeys>
+__device__ void next_item(const Attn &p, int R, Item &it) {
+    it.first += it.units;
+    if ((it.qt + 1) * R < it.s.nq * p.G) {
+        ++it.qt;
+    } else {
+        it.qt = 0;
+        if (++it.h == p.c.Hkv) {
+            it.h = 0;
+            do it.s = seq_of(p.b, ++it.b, p.ctrl);
+            while (it.s.nq == 0);
+        }
+    }
+    it.units = tile_units<kKeys>(it.s, p.G, R, it.qt);
 }
 
 __device__ inline uint32_t bf16x2_of(float a, float b) {

@@ -94,8 +94,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 2) kv4_decode_kern
     if (c >= C) return;
     const long long u_end = U * (c + 1) / C;
 
-    for (long long u = U * c / C; u < u_end;) {
-        const Item it = find_item<kStep>(p, R, s_pre, u);
+    long long u = U * c / C;
+    if (u >= u_end) return;
+    for (Item it = find_item<kStep>(p, R, s_pre, u); ; next_item<kStep>(p, R, it)) {
         const int st0 = (int)(u - it.first), st1 = (int)min((long long)it.units, u_end - it.first);
         const int rows = min(R, it.s.nq * p.G - it.qt * R);
 
@@ -359,6 +360,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 2) kv4_decode_kern
             __syncthreads();
         }
         u = it.first + st1;
+        if (u >= u_end) break;
     }
 }
 
