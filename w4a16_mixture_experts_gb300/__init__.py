@@ -17,7 +17,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import NamedTuple
 
 import torch
 
@@ -121,8 +120,14 @@ def _p(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# The current stream's handle, without a Stream object around it where PyTorch has the call.
+_raw_stream, _device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None and _device is not None:
+            return _raw_stream(_device())
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream))
 
@@ -401,14 +406,34 @@ def moe_w8a16_workspace_size(T: int, N: int, K: int, gs: int) -> int:
     return n.value
 
 
-class Kv4Cache(NamedTuple):
+class Kv4Cache:
     """One layer's paged 4-bit KV cache: codes int32 [pages, Hkv, page_size, D/8] (q + 8, eight to a
     word, lowest nibble first) and scales bf16 [pages, Hkv, page_size], of K and of V. The slot of a
-    token is page * page_size + its place in the page."""
-    k_codes: torch.Tensor
-    k_scales: torch.Tensor
-    v_codes: torch.Tensor
-    v_scales: torch.Tensor
+    token is page * page_size + its place in the page. Iterates over its four tensors."""
+    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "_c")
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales):
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self._c = None
+
+    def __iter__(self):
+        return iter((self.k_codes, self.k_scales, self.v_codes, self.v_scales))
+
+    def c(self) -> moe_kv4_cache:
+        """The C struct, formed (and the tensors checked) anew where a tensor's memory has moved."""
+        kc, ks, vc, vs = self.k_codes, self.k_scales, self.v_codes, self.v_scales
+        at = (kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), kc.shape)
+        if self._c is None or self._c[0] != at:
+            _need(kc, "k_codes", torch.int32, 4)
+            _need(ks, "k_scales", torch.bfloat16, 3)
+            _need(vc, "v_codes", torch.int32, 4)
+            _need(vs, "v_scales", torch.bfloat16, 3)
+            n, h, p, w = kc.shape
+            if vc.shape != kc.shape or ks.shape != (n, h, p) or vs.shape != (n, h, p):
+                raise ValueError("a cache holds codes [pages, Hkv, page_size, D/8] and scales [pages, Hkv, page_size], "
+                                 "got %s %s %s %s" % tuple(tuple(t.shape) for t in self))
+            self._c = at, moe_kv4_cache(*at[:4], n, h, p, w * 8), h, w * 8
+        return self._c
 
 
 def kv4_cache(n_pages: int, Hkv: int, page_size: int, D: int, device=None) -> Kv4Cache:
@@ -433,20 +458,31 @@ def kv4_workspace(T: int = 0, Hq: int = 1, Hkv: int = 1, D: int = 128, device=No
     return torch.zeros(n, dtype=torch.uint8, device=device if device is not None else "cuda")
 
 
-def _heads(t, name, T=None, D=None):
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+_strides = {}   # (token, head) -> the struct: few pairs occur, and forming one costs more than finding it
+
+
+def _heads(t, name, T=None, heads=None, D=None):
     """The strides of a bf16 [T, heads, D] CUDA tensor with contiguous D."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     shape = t.shape
-    if t.dtype != torch.bfloat16 or len(shape) != 3 or (T is not None and shape[0] != T) or (
-            D is not None and shape[2] != D):
-        raise ValueError("%s must be bf16 [%s, heads, %s], got %s %s" % (
-            name, "T" if T is None else T, "D" if D is None else D, t.dtype, tuple(shape)))
-    st = t.stride()
-    if not t.is_cuda or (st[2] != 1 and shape[2] > 1):
+    if t.dtype != _BF16 or len(shape) != 3 or (T is not None and shape[0] != T) or (
+            heads is not None and shape[1] != heads) or (D is not None and shape[2] != D):
+        raise ValueError("%s must be bf16 [%s, %s, %s], got %s %s" % (
+            name, "T" if T is None else T, "heads" if heads is None else heads, "D" if D is None else D, t.dtype,
+            tuple(shape)))
+    token, head, one = t.stride()
+    if not t.is_cuda or (one != 1 and shape[2] > 1):
         raise ValueError("%s must be a CUDA tensor with contiguous head values" % name)
     # (a dimension of one entry has no stride that matters)
-    return moe_strides(st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0)
+    key = (token if shape[0] > 1 else 0, head if shape[1] > 1 else 0)
+    st = _strides.get(key)
+    if st is None:
+        if len(_strides) > 4096:
+            _strides.clear()
+        st = _strides[key] = moe_strides(*key)
+    return st
 
 
 def _vec(t, name, dtype, n=None):
@@ -458,17 +494,9 @@ def _vec(t, name, dtype, n=None):
     return t.data_ptr()
 
 
-def _cache(c) -> moe_kv4_cache:
-    kc, ks, vc, vs = c
-    _need(kc, "k_codes", torch.int32, 4)
-    _need(ks, "k_scales", torch.bfloat16, 3)
-    _need(vc, "v_codes", torch.int32, 4)
-    _need(vs, "v_scales", torch.bfloat16, 3)
-    n, h, p, w = kc.shape
-    if vc.shape != kc.shape or ks.shape != (n, h, p) or vs.shape != (n, h, p):
-        raise ValueError("a cache holds codes [pages, Hkv, page_size, D/8] and scales [pages, Hkv, page_size], got %s %s %s %s"
-                         % tuple(tuple(t.shape) for t in c))
-    return moe_kv4_cache(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), n, h, p, w * 8)
+def _cache(c):
+    """(C struct, KV heads, D) of a Kv4Cache, or of four tensors in its order."""
+    return (c if isinstance(c, Kv4Cache) else Kv4Cache(*c)).c()[1:]
 
 
 def moe_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -482,14 +510,13 @@ def moe_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, ep
     """
     qs = _heads(q, "q")
     T, Hq, D = q.shape
-    ks = _heads(k, "k", T, D)
+    ks = _heads(k, "k", T, None, D)
+    Hkv = k.shape[1]
     if q_out is None:
-        q_out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device)
+        q_out = torch.empty(T, Hq, D, dtype=_BF16, device=q.device)
     if k_out is None:
-        k_out = torch.empty(T, k.shape[1], D, dtype=torch.bfloat16, device=q.device)
-    qos, kos = _heads(q_out, "q_out", T, D), _heads(k_out, "k_out", T, D)
-    if q_out.shape[1] != Hq or k_out.shape[1] != k.shape[1]:
-        raise ValueError("q_out and k_out must have the heads of q and k")
+        k_out = torch.empty(T, Hkv, D, dtype=_BF16, device=q.device)
+    qos, kos = _heads(q_out, "q_out", T, Hq, D), _heads(k_out, "k_out", T, Hkv, D)
     pos = fr = None
     rot = 0
     if inv_freq is not None:
@@ -499,7 +526,7 @@ def moe_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, ep
                                   None if q_weight is None else _vec(q_weight, "q_weight", torch.bfloat16, D),
                                   None if k_weight is None else _vec(k_weight, "k_weight", torch.bfloat16, D),
                                   pos, fr, rot, 1 if interleaved else 0, eps, q_out.data_ptr(), qos, k_out.data_ptr(),
-                                  kos, T, Hq, k.shape[1], D, _stream(stream)), "moe_qk_norm_rope")
+                                  kos, T, Hq, Hkv, D, _stream(stream)), "moe_qk_norm_rope")
     return q_out, k_out
 
 
@@ -507,12 +534,10 @@ def moe_kv4_append(k, v, slots, cache: Kv4Cache, ws=None, stream=None):
     """Quantises token t's rows k[t], v[t] (bf16 [T, Hkv, D], views allowed) into the cache at
     slots[t] (int32 [T]; -1: not stored). ws: kv4_workspace(), whose error word
     moe_check_device_error reads. Returns the cache."""
-    c = _cache(cache)
-    ks = _heads(k, "k", None, c.D)
+    c, Hkv, D = _cache(cache)
+    ks = _heads(k, "k", None, Hkv, D)
     T = k.shape[0]
-    vs = _heads(v, "v", T, c.D)
-    if k.shape[1] != c.Hkv or v.shape[1] != c.Hkv:
-        raise ValueError("k and v must have the cache's %d heads, got %d and %d" % (c.Hkv, k.shape[1], v.shape[1]))
+    vs = _heads(v, "v", T, Hkv, D)
     if ws is None:
         ws = kv4_workspace(device=k.device)
     _check(lib().moe_kv4_append(k.data_ptr(), ks, v.data_ptr(), vs, _vec(slots, "slots", torch.int32, T), T, c,
@@ -522,9 +547,9 @@ def moe_kv4_append(k, v, slots, cache: Kv4Cache, ws=None, stream=None):
 
 def moe_kv4_read(slots, cache: Kv4Cache, k_out=None, v_out=None, ws=None, stream=None):
     """The cache's rows at slots (int32 [T]; -1 reads as zero) as bf16 values: (k, v) [T, Hkv, D]."""
-    c = _cache(cache)
+    c, Hkv, D = _cache(cache)
     at = _vec(slots, "slots", torch.int32)
-    shape = (slots.shape[0], c.Hkv, c.D)
+    shape = (slots.shape[0], Hkv, D)
     if k_out is None:
         k_out = torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
     if v_out is None:
@@ -549,9 +574,9 @@ def moe_kv4_attention(q, cache: Kv4Cache, page_table, lens, cu_q=None, max_q: in
     max_q is the largest number of queries of a sequence. scale defaults to D ** -0.5.
     ws: kv4_workspace(T, Hq, Hkv, D). Returns out, or (out, lse f32 [T, Hq]) where lse is given
     (a tensor, or True to have it made)."""
-    c = _cache(cache)
-    qs = _heads(q, "q", None, c.D)
-    T, Hq, D = q.shape
+    c, Hkv, D = _cache(cache)
+    qs = _heads(q, "q", None, None, D)
+    T, Hq = q.shape[0], q.shape[1]
     B = lens.shape[0]
     at = _vec(lens, "lens", torch.int32)
     cu = None if cu_q is None else _vec(cu_q, "cu_q", torch.int32, B + 1)
@@ -560,15 +585,15 @@ def moe_kv4_attention(q, cache: Kv4Cache, page_table, lens, cu_q=None, max_q: in
         raise ValueError("page_table must have a row for each of the %d sequences, got %s" % (B, tuple(page_table.shape)))
     if out is None:
         out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device)
-    os_ = _heads(out, "out", T, D)
+    os_ = _heads(out, "out", T, Hq, D)
     if lse is True:
         lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
     if lse is not None:
-        _need(lse, "lse", torch.float32, 2)
-    if out.shape[1] != Hq or (lse is not None and lse.shape != (T, Hq)):
-        raise ValueError("out must be [T, Hq, D] and lse [T, Hq]")
+        _need(lse, "lse", _F32, 2)
+        if lse.shape != (T, Hq):
+            raise ValueError("lse must be [%d, %d], got %s" % (T, Hq, tuple(lse.shape)))
     if ws is None:
-        ws = kv4_workspace(T, Hq, c.Hkv, D, device=q.device)
+        ws = kv4_workspace(T, Hq, Hkv, D, device=q.device)
     _check(lib().moe_kv4_attention(q.data_ptr(), qs, c, page_table.data_ptr(), page_table.shape[1], at, cu, B, T, Hq,
                                    max_q, D ** -0.5 if scale is None else scale, out.data_ptr(), os_,
                                    None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
