@@ -320,7 +320,8 @@ typedef struct {
  * nibble first, its scale one bf16, and its values q * scale.
  *   k_codes, v_codes   int32 [n_pages][Hkv][page_size][D/8]
  *   k_scales, v_scales bf16  [n_pages][Hkv][page_size]
- * page_size is a power of two from 16 to 1024; n_pages * page_size < 2^31. The
+ * page_size is a power of two from 16 to 1024; n_pages * page_size < 2^31 and
+ * n_pages * page_size * Hkv < 2^32 - 1; Hkv is at most 1024. The
  * slot of a token is page * page_size + its place in the page. A scale that is
  * not finite marks a row that held a value that was not: every query that
  * sees the row, and no other, gets NaN.

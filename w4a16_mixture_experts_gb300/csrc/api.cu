@@ -351,6 +351,8 @@ int check_cache(const moe_kv4_cache &c) {
     if (c.D != 64 && c.D != 128) return MOE_ERR_UNSUPPORTED;
     if (c.page_size < 16 || c.page_size > 1024 || (c.page_size & (c.page_size - 1))) return MOE_ERR_UNSUPPORTED;
     if ((int64_t)c.n_pages * c.page_size >= ((int64_t)1 << 31) || c.Hkv > 1024) return MOE_ERR_UNSUPPORTED;
+    // row indexes fit 32 bits (more rows than that do not fit the memory)
+    if ((int64_t)c.n_pages * c.page_size * c.Hkv >= ((int64_t)1 << 32) - 1) return MOE_ERR_UNSUPPORTED;
     if (!ptr_ok(c.k_codes, false) || !ptr_ok(c.k_scales, false) || !ptr_ok(c.v_codes, false) ||
         !ptr_ok(c.v_scales, false))
         return MOE_ERR_INVALID_ARG;

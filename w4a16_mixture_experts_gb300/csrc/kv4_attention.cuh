@@ -52,6 +52,24 @@ struct Attn {
 // its values, and the rows' values.
 __host__ __device__ constexpr int part_floats(int R, int D) { return 2 * R + 4 + R * D; }
 
+// Loads of the cache that stay where they are written (the compiler would move
+// them down to their first use, and their latency with them), past the L1.
+__device__ inline uint4 ld_stream(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ inline uint16_t ld_here(const uint16_t *p) {
+    uint16_t v;
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+}
+__device__ inline int ld_here(const int32_t *p) {
+    int v;
+    asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
 __device__ inline float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -100,9 +118,9 @@ __device__ inline int tile_units(const Seq &s, int G, int R, int qt) {
 
 // pre[b] = units of the sequences before b, for all of them: every CTA forms
 // it, a thread a sequence (a warp, for a sequence of many row tiles). Returns
-// the total.
+// the total, below 2^31 (more is refused as a value out of range).
 template <int kThreads, int kKeys>
-__device__ long long scan_units(const Attn &p, int R, long long *pre, long long *warp_sums) {
+__device__ int scan_units(const Attn &p, int R, int *pre, long long *warp_sums) {
     long long base = 0;
     for (int b0 = 0; b0 < p.b.B; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
@@ -136,24 +154,40 @@ __device__ long long scan_units(const Attn &p, int R, long long *pre, long long 
             if (w < (int)(threadIdx.x >> 5)) before += warp_sums[w];
             base += warp_sums[w];
         }
-        if (b < p.b.B) pre[b] = before + inc - n;
-        __syncthreads();
+        if (b < p.b.B) pre[b] = (int)(before + inc - n);
+        if (b0 + kThreads < p.b.B) __syncthreads();
     }
-    if (threadIdx.x == 0) pre[p.b.B] = base;
+    if (threadIdx.x == 0) pre[p.b.B] = (int)base;
     __syncthreads();
-    return base;
+    if (base >= (1ll << 31)) {
+        set_error(p.ctrl, MOE_ERR_DEVICE);
+        return 0;
+    }
+    return (int)base;
 }
+
+// The shares of C CTAs in U units: CTA c begins at floor(U c / C).
+struct Shares {
+    int U, C, q, r;
+    __device__ Shares(int units, int ctas) : U(units), C(ctas), q(units / ctas), r(units % ctas) {}
+    __device__ int begin(int c) const { return q * c + r * c / C; }
+    __device__ int holder(int u) const {   // the CTA whose share holds unit u
+        int c = (int)((float)u * (float)C / (float)U);
+        while (begin(c + 1) <= u) ++c;
+        while (begin(c) > u) --c;
+        return c;
+    }
+};
 
 struct Item {
     int b, h, qt;
-    int units;            // of the item
-    long long first;      // its first unit
+    int units, first;     // of the item; its first unit
     Seq s;
 };
 
 // The item that holds unit u (u below the total); a whole warp calls it.
 template <int kKeys>
-__device__ Item find_item(const Attn &p, int R, const long long *pre, long long u) {
+__device__ Item find_item(const Attn &p, int R, const int *pre, int u) {
     Item it;
     int lo = 0;
     for (int hi = p.b.B; hi - lo > 1;) {
@@ -163,9 +197,9 @@ __device__ Item find_item(const Attn &p, int R, const long long *pre, long long 
     }
     it.b = lo;   // (sequences without units share their successor's pre: the last of them is the one)
     it.s = seq_of(p.b, lo, p.ctrl);
-    const long long per_head = (pre[lo + 1] - pre[lo]) / p.c.Hkv;
-    it.h = (int)((u - pre[lo]) / per_head);
-    long long at = pre[lo] + it.h * per_head;
+    const int per_head = (pre[lo + 1] - pre[lo]) / p.c.Hkv;
+    it.h = (u - pre[lo]) / per_head;
+    int at = pre[lo] + it.h * per_head;
     const int tiles = (it.s.nq * p.G + R - 1) / R, lane = threadIdx.x & 31;
     for (int q0 = 0;; q0 += 32) {   // 32 row tiles at a time
         const int n = q0 + lane < tiles ? tile_units<kKeys>(it.s, p.G, R, q0 + lane) : 0;
@@ -253,9 +287,6 @@ __device__ void join_parts(const Attn &p, const Item &it, int rows, int c0, int 
         write_row4(p, it, R, r, d, acc, M, L, F);
     }
 }
-
-// The CTA whose share holds unit u.
-__device__ inline int cta_of(long long u, long long U, int C) { return (int)(((u + 1) * C - 1) / U); }
 
 }  // namespace kv4
 }  // namespace moe

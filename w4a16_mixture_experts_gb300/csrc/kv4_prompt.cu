@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
     extern __shared__ uint8_t s_dyn[];
     uint8_t *const sQ = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(s_dyn) + 1023) & ~(uintptr_t)1023);
     uint8_t *const sK = sQ + 2 * Cfg::kTile, *const sV = sK + kStages * Cfg::kTile;
-    long long *const s_pre = reinterpret_cast<long long *>(sV + kStages * Cfg::kTile);
+    int *const s_pre = reinterpret_cast<int *>(sV + kStages * Cfg::kTile);
     __shared__ Bars bars;
     __shared__ long long s_sums[kThreads / 32];
     __shared__ uint32_t s_tmem;
@@ -196,11 +196,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
     }
     pdl_wait();
     pdl_launch_dependents();
-    const long long U = scan_units<kThreads, kKeys>(p, kR, s_pre, s_sums);
-    const int C = (int)min((long long)gridDim.x, max(1LL, U));
+    const int U = scan_units<kThreads, kKeys>(p, kR, s_pre, s_sums);
+    const Shares shares(U, min((int)gridDim.x, max(1, U)));
     const int c = blockIdx.x;
-    if (c >= C || U == 0) return;   // (the whole CTA)
-    const long long u_begin = U * c / C, u_end = U * (c + 1) / C;
+    if (c >= shares.C || U == 0) return;   // (the whole CTA)
+    const int u_begin = shares.begin(c), u_end = shares.begin(c + 1);
     if (warp == kWMma) {
         tc::alloc(&s_tmem, 512);
         tc::relinquish();
@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
         uint32_t g = 0, gs = 0, n_item = 0;   // stages so far (all items; of this tile's), items
         bool ok = true;
         Item it = find_item<kKeys>(p, kR, s_pre, u_begin);
-        for (long long u = u_begin;; next_item<kKeys>(p, kR, it), ++n_item) {
-            const int st0 = (int)(u - it.first), st1 = (int)min((long long)it.units, u_end - it.first);
+        for (int u = u_begin;; next_item<kKeys>(p, kR, it), ++n_item) {
+            const int st0 = u - it.first, st1 = min(it.units, u_end - it.first);
             const int rows = min(kR, it.s.nq * p.G - it.qt * kR);
             const int rr = it.qt * kR + r, qi = rr / p.G, head = it.h * p.G + rr - qi * p.G;
             const bool mine = wg * kTileRows < rows;   // (the whole warpgroup) this tile has rows
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
             tc::fence_before();
             if (!whole) {
                 ok = bar_and(1, 256, ok);
-                const int c0 = cta_of(it.first, U, C), c1 = cta_of(it.first + it.units - 1, U, C);
+                const int c0 = shares.holder(it.first), c1 = shares.holder(it.first + it.units - 1);
                 if (ok && threadIdx.x == 0) {
                     __threadfence();
                     const uint32_t n = atom_acq_rel_add_u32(p.ticket + c0, 1u);
@@ -398,8 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
         uint32_t g = 0;
         bool ok = true;
         Item it = find_item<kKeys>(p, kR, s_pre, u_begin);
-        for (long long u = u_begin; ok; next_item<kKeys>(p, kR, it)) {
-            const int st0 = (int)(u - it.first), st1 = (int)min((long long)it.units, u_end - it.first);
+        for (int u = u_begin; ok; next_item<kKeys>(p, kR, it)) {
+            const int st0 = u - it.first, st1 = min(it.units, u_end - it.first);
             const int32_t *table = p.b.table + (size_t)it.b * p.b.max_pages;
             const int len = it.s.len, pmask = (1 << p.b.shift) - 1;
             auto page_of = [&](int st) {
@@ -521,8 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                 __syncwarp();
             };
             Item it = find_item<kKeys>(p, kR, s_pre, u_begin);
-            for (long long u = u_begin;; next_item<kKeys>(p, kR, it), ++n_item) {
-                const int st0 = (int)(u - it.first), st1 = (int)min((long long)it.units, u_end - it.first);
+            for (int u = u_begin;; next_item<kKeys>(p, kR, it), ++n_item) {
+                const int st0 = u - it.first, st1 = min(it.units, u_end - it.first);
                 const bool two = it.s.nq * p.G - it.qt * kR > kTileRows;
                 ok = wait(&bars.q_full, n_item & 1, abort_flag) && wait(&bars.k_full[g % kStages], (g / kStages) & 1, abort_flag);
                 if (ok) {
@@ -586,11 +586,11 @@ cudaError_t launch_one(const Attn &p, cudaStream_t s) {
     }();
     if (!split_ok) return cudaErrorInvalidConfiguration;
     constexpr size_t kBase = PromptCfg<D>::kSmem + 1024;
-    const cudaError_t err = set_smem_once(fn, (int)(kBase + sizeof(long long) * 4097));
+    const cudaError_t err = set_smem_once(fn, (int)(kBase + sizeof(int) * 4097));
     if (err != cudaSuccess) return err;
     int grid = sm_count();
     if (grid > kMaxPromptCtas) grid = kMaxPromptCtas;
-    return launch_pdl(kv4_prompt_kernel<D>, dim3((unsigned)grid), kThreads, kBase + sizeof(long long) * ((size_t)p.b.B + 1), s, p);
+    return launch_pdl(kv4_prompt_kernel<D>, dim3((unsigned)grid), kThreads, kBase + sizeof(int) * ((size_t)p.b.B + 1), s, p);
 }
 
 }  // namespace
