@@ -5,9 +5,10 @@
 // is query r / G, head r % G of the group. Its work is a number of units, each a
 // fixed count of keys. All items' units lie one after another and CTA c of C
 // takes the units [U c / C, U (c + 1) / C), whatever items they belong to: an
-// even share for any mix of lengths. An item that lies in several CTAs' shares
-// is joined by the last of them to finish, in the CTAs' order, so that the
-// result does not depend on which that is.
+// even share for any mix of lengths. The parts of an item that lies in several
+// CTAs' shares are joined, in the CTAs' order, by a second kernel, which the
+// whole card runs. (The last of the CTAs to finish joining them alone took up to
+// 60 us of a prompt chunk's 180, and its fence and ticket 1 us of the others.)
 #pragma once
 
 #include <cuda_fp16.h>
@@ -28,11 +29,17 @@ constexpr int kPromptRows = 256;
 
 // Partial results of at most so many CTAs; fixed figures, so that the
 // workspace's size does not depend on the device (152 SMs; the streaming kernel
-// runs two CTAs on each).
-constexpr int kMaxCtas = 320, kMaxPromptCtas = 160;
-// The tickets lie in the workspace's first region that calls leave at zero.
-constexpr size_t kTicketOff = 512, kPartOff = 512 + (size_t)kMaxE * kCtrStride * 4;
-static_assert((size_t)kMaxCtas * 4 <= kPartOff - kTicketOff, "tickets");
+// runs up to four CTAs on each).
+constexpr int kMaxCtas = 640, kMaxPromptCtas = 160;
+// The parts and what joins them lie behind the regions that calls leave at
+// zero, so that a workspace may serve the experts' calls too.
+constexpr size_t kPartOff = 512 + (size_t)kMaxE * kCtrStride * 4;
+
+// What a CTA leaves for the join: the item that it began and did not finish
+// goes on to CTA `last` (0: there is none such).
+struct Begun {
+    int last, q0, h, qt, rows, pad[3];
+};
 
 struct Attn {
     Batch b;
@@ -42,8 +49,8 @@ struct Attn {
     uint16_t *out;
     float *lse;
     Ctrl *ctrl;
-    uint32_t *ticket;   // [kMaxCtas]
-    float *part;        // [CTAs][2] x part_floats(R, D)
+    Begun *begun;       // [CTAs]
+    float *part;        // [CTAs][2] x part_floats(R, D): a CTA's first part continues an item, its second begins one
     float scale;
     int Hq, G;
 };
@@ -185,6 +192,31 @@ struct Item {
     Seq s;
 };
 
+// The row tile of a sequence and head (whose units begin at `at`) that holds unit u; a
+// whole warp calls it.
+template <int kKeys>
+__device__ void find_tile(const Attn &p, int R, int u, int at, Item &it) {
+    const int tiles = (it.s.nq * p.G + R - 1) / R, lane = threadIdx.x & 31;
+    for (int q0 = 0;; q0 += 32) {   // 32 at a time
+        const int n = q0 + lane < tiles ? tile_units<kKeys>(it.s, p.G, R, q0 + lane) : 0;
+        int inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        const uint32_t here = __ballot_sync(0xffffffffu, u < at + inc);
+        if (here || q0 + 32 >= tiles) {
+            const int src = here ? __ffs(here) - 1 : 0;
+            it.qt = q0 + src;
+            it.units = __shfl_sync(0xffffffffu, n, src);
+            it.first = at + __shfl_sync(0xffffffffu, inc - n, src);
+            return;
+        }
+        at += __shfl_sync(0xffffffffu, inc, 31);
+    }
+}
+
 // The item that holds unit u (u below the total); a whole warp calls it.
 template <int kKeys>
 __device__ Item find_item(const Attn &p, int R, const int *pre, int u) {
@@ -199,26 +231,80 @@ __device__ Item find_item(const Attn &p, int R, const int *pre, int u) {
     it.s = seq_of(p.b, lo, p.ctrl);
     const int per_head = (pre[lo + 1] - pre[lo]) / p.c.Hkv;
     it.h = (u - pre[lo]) / per_head;
-    int at = pre[lo] + it.h * per_head;
-    const int tiles = (it.s.nq * p.G + R - 1) / R, lane = threadIdx.x & 31;
-    for (int q0 = 0;; q0 += 32) {   // 32 row tiles at a time
-        const int n = q0 + lane < tiles ? tile_units<kKeys>(it.s, p.G, R, q0 + lane) : 0;
-        int inc = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += v;
-        }
-        const uint32_t here = __ballot_sync(0xffffffffu, u < at + inc);
-        if (here || q0 + 32 >= tiles) {
-            const int src = here ? __ffs(here) - 1 : 0;
-            it.qt = q0 + src;
-            it.units = __shfl_sync(0xffffffffu, n, src);
-            it.first = at + __shfl_sync(0xffffffffu, inc - n, src);
-            return it;
-        }
-        at += __shfl_sync(0xffffffffu, inc, 31);
+    const int at = pre[lo] + it.h * per_head;
+    find_tile<kKeys>(p, R, u, at, it);
+    return it;
+}
+
+// The shares, and the first item of CTA c's (where it has one: c < C). Up to
+// kThreads sequences, the thread that has the item's sequence in its registers
+// passes it on; beyond that it is searched for. Ends with the item in every
+// thread, but not with a barrier.
+template <int kThreads, int kKeys>
+__device__ Shares first_item(const Attn &p, int R, int c, int *pre, long long *warp_sums, Item &shared, Item &it) {
+    if (p.b.B > kThreads) {
+        const int U = scan_units<kThreads, kKeys>(p, R, pre, warp_sums);
+        Shares shares(U, U == 0 ? 1 : min((int)gridDim.x, U));
+        if (U == 0) shares.C = 0;
+        if (c < shares.C) it = find_item<kKeys>(p, R, pre, shares.begin(c));
+        return shares;
     }
+    const int b = threadIdx.x, lane = threadIdx.x & 31;
+    Seq s{0, 0, 0};
+    if (b < p.b.B) s = seq_of(p.b, b, p.ctrl);
+    const int tiles = (s.nq * p.G + R - 1) / R;
+    long long per_head = 0;
+    if (tiles <= 2)
+        for (int qt = 0; qt < tiles; ++qt) per_head += tile_units<kKeys>(s, p.G, R, qt);
+    for (uint32_t many = __ballot_sync(0xffffffffu, tiles > 2); many; many &= many - 1) {
+        const int src = __ffs(many) - 1;
+        const Seq o{0, __shfl_sync(0xffffffffu, s.nq, src), __shfl_sync(0xffffffffu, s.len, src)};
+        const int ot = (o.nq * p.G + R - 1) / R;
+        long long m = 0;
+        for (int qt = lane; qt < ot; qt += 32) m += tile_units<kKeys>(o, p.G, R, qt);
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) m += __shfl_xor_sync(0xffffffffu, m, x);
+        if (lane == src) per_head = m;
+    }
+    const long long n = per_head * p.c.Hkv;
+    long long inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) warp_sums[threadIdx.x >> 5] = inc;
+    __syncthreads();
+    long long total = 0, before = inc - n;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < (int)(threadIdx.x >> 5)) before += warp_sums[w];
+        total += warp_sums[w];
+    }
+    if (total >= (1ll << 31)) {
+        set_error(p.ctrl, MOE_ERR_DEVICE);
+        total = 0;
+    }
+    Shares shares((int)total, total == 0 ? 1 : (int)min((long long)gridDim.x, total));
+    if (total == 0) shares.C = 0;
+    if (c < shares.C) {
+        const int u = shares.begin(c);
+        const bool mine = before <= u && u < before + n;
+        const uint32_t who = __ballot_sync(0xffffffffu, mine);
+        if (who) {   // (one warp) its lanes look through the sequence's row tiles
+            const int src = __ffs(who) - 1;
+            const int ph = (int)__shfl_sync(0xffffffffu, per_head, src), at0 = (int)__shfl_sync(0xffffffffu, before, src);
+            Item x;
+            x.b = (threadIdx.x & ~31) + src;
+            x.s = Seq{__shfl_sync(0xffffffffu, s.q0, src), __shfl_sync(0xffffffffu, s.nq, src), __shfl_sync(0xffffffffu, s.len, src)};
+            x.h = (u - at0) / ph;
+            find_tile<kKeys>(p, R, u, at0 + x.h * ph, x);
+            if (lane == 0) shared = x;
+        }
+        __syncthreads();
+        it = shared;
+    }
+    return shares;
 }
 
 // The item after `it`, where there is one.
@@ -241,51 +327,6 @@ __device__ void next_item(const Attn &p, int R, Item &it) {
 __device__ inline uint32_t bf16x2_of(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-// Four finished values of row r of an item (and the row's log-sum-exp): value
-// times 2^(F - 127) over the row's sum; a row without a key is zero.
-__device__ inline void write_row4(const Attn &p, const Item &it, int R, int r, int d, float4 v, float m, float l, int F) {
-    const int rr = it.qt * R + r, i = rr / p.G, head = it.h * p.G + rr - i * p.G;
-    const size_t tok = (size_t)(it.s.q0 + i);
-    const float inv = l == 0.f ? 0.f : 1.f / l, up = pow2_biased(F);
-    *reinterpret_cast<uint2 *>(p.out + tok * p.os.token + (size_t)head * p.os.head + d) =
-        make_uint2(bf16x2_of(v.x * inv * up, v.y * inv * up), bf16x2_of(v.z * inv * up, v.w * inv * up));
-    if (d == 0 && p.lse) p.lse[tok * p.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-}
-
-// Joins the parts of an item that CTAs c0 .. c1 left, in their order: the
-// first is its CTA's last part, the others are their CTAs' first.
-template <int kThreads, int R, int D>
-__device__ void join_parts(const Attn &p, const Item &it, int rows, int c0, int c1) {
-    constexpr int N = part_floats(R, D);
-    auto at = [&](int c) { return p.part + (size_t)(c * 2 + (c == c0)) * N; };
-    for (int x = threadIdx.x; x < rows * (D / 4); x += kThreads) {
-        const int r = x / (D / 4), d = (x % (D / 4)) * 4;
-        float M = kNoMax, L = 0.f;
-        int F = 1;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) {
-            const float *q = at(c);
-            const float m = __ldcg(q + r), l = __ldcg(q + R + r);
-            const int f = __float_as_int(__ldcg(q + 2 * R));
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(q + 2 * R + 4 + r * D + d));
-            const float Mn = fmaxf(M, m);
-            const int Fn = max(F, f);
-            const float a = exp2_approx(M - Mn), b = exp2_approx(m - Mn);
-            const float av = Fn - F > 126 ? 0.f : a * pow2_biased(127 + F - Fn);
-            const float bv = Fn - f > 126 ? 0.f : b * pow2_biased(127 + f - Fn);
-            L = L * a + l * b;
-            acc.x = acc.x * av + v.x * bv;
-            acc.y = acc.y * av + v.y * bv;
-            acc.z = acc.z * av + v.z * bv;
-            acc.w = acc.w * av + v.w * bv;
-            M = Mn;
-            F = Fn;
-        }
-        write_row4(p, it, R, r, d, acc, M, L, F);
-    }
 }
 
 }  // namespace kv4

@@ -30,6 +30,8 @@
 // far (a power of two, put back at the end), so that no range of scales is lost.
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "kv4_attention.cuh"
 #include "tcgen05.cuh"
 
@@ -44,54 +46,61 @@ constexpr uint32_t kNibs = 0x0F0F0F0Fu;
 
 template <int D, int R>
 struct DecodeCfg {
-    static constexpr int kGroups = 2;                     // warpgroups a CTA
-    static constexpr int kPerSm = R < 32 ? 2 : 1;         // CTAs an SM: 128 registers a thread, or 255 for the most rows
-    static constexpr int kThreads = kGroups * 128;
-    static constexpr int kStride = D + 4;                 // of a row of partial values in shared memory
+    static constexpr int kThreads = 128;                  // a warpgroup
+    static constexpr int kPerSm = R < 16 ? 4 : 3;         // CTAs an SM
     static constexpr int kNS = 2 * R, kNP = R < 16 ? 16 : R;   // columns of S^T (two a row) and of O^T (R = 8: twice the same)
-    static constexpr int kV = 128 * D * 2, kP = R * 256;  // bytes of a warpgroup's operands
-    static constexpr int kPs = R == 16 ? 1 : 2;           // of P: two where they fit, one read while the next is written
+    static constexpr int kV = 128 * D * 2, kP = R * 256;  // bytes of the operands
+    static constexpr int kPs = R < 32 ? 2 : 1;            // of P: two where they fit, one read while the next is written
     static constexpr int kQ = kNS * 128;
-    static constexpr int kWarpRaw = 32 * D / 2, kRaw = 4 * kWarpRaw;   // a warp's codes of 32 keys (K or V), a warpgroup's
-    // tensor memory of a warpgroup: K's row, scores, values' sums
+    static constexpr int kWarpRaw = 32 * D / 2, kRaw = 4 * kWarpRaw;   // codes of a warp's 32 keys (K or V), of all
+    // tensor memory: K's row, scores, values' sums
     static constexpr int kColS = 32, kColO = kColS + kNS, kCols = R < 16 ? 64 : 128;
     static_assert(kColO + kNP <= kCols, "tensor memory");
-    static constexpr int kGroup = kV + kPs * kP + 2 * kRaw, kSmem = kQ + kGroups * kGroup;
+    static constexpr int kSmem = kQ + kV + kPs * kP + 2 * kRaw;
     static constexpr int kChunks = D / 32;                // 16-byte pieces of a row of codes
-    static_assert(R * kStride * 4 <= kV, "the rows' parts lie where V was");
 };
 
-struct Bars {
-    uint64_t s_full[2], o_full[2];   // of each warpgroup: scores formed, values added
-};
-
-template <int W, int R>
+template <int R>
 struct DecodeShared {
-    alignas(16) float c[R], base[R], m[W][R], l[W][R], wm[W][4][R];
-    alignas(16) uint16_t scales[W * 4][3][2][32];   // of a warp's units in turn: K's, V's
-    Bars bars;
-    long long sums[W * 4];
-    int lim[R], F[W], we[W][4], fail[W], last;
+    alignas(16) float c[R], base[R], m[R], wm[4][R];
+    alignas(16) uint16_t scales[4][3][2][32];   // of a warp's units in turn: K's, V's
+    uint64_t s_full, o_full;                    // scores formed, values added
+    long long sums[4];
+    Item first;
+    int lim[R], we[4];
     uint32_t tmem;
 };
 
+// Bounded wait on a phase. The hint lets a warp sleep through most of a wait (a
+// poll returns after 20 us at the latest; the default hint polls about every 40
+// clocks, and the other warps pay for it).
 __device__ inline bool wait(uint64_t *bar, uint32_t parity) {
-    bool ok = false;
-    for (uint32_t i = 0; i < kSpinLimit && !ok; ++i) ok = mbar_try_wait(bar, parity);
-    return __all_sync(0xffffffffu, ok);
+    uint32_t ok = 0;
+    for (uint32_t i = 0; i < (1u << 15) && !ok; ++i)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+    return ok != 0;
 }
 
-// Named barrier of a warpgroup, and the same returning the OR of v.
-__device__ inline void bar_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
-__device__ inline bool bar_or(int id, bool v) {
+// The CTA's barrier, returning the OR of v; and one that all but warp 0 only pass by.
+__device__ inline bool bar_or(bool v) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        "barrier.cta.red.or.pred q, 0, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)v), "r"(id)
+        : "r"((uint32_t)v)
         : "memory");
     return r != 0;
+}
+__device__ inline void bar_pass(int warp) {
+    if (warp == 0) asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+    else asm volatile("barrier.cta.arrive 1, 128;" ::: "memory");
 }
 
 __device__ inline bool elect() {
@@ -216,9 +225,9 @@ __device__ inline void reduce_rows(const float (&v)[R], float *to) {
     if ((lane & (32 / R - 1)) == 0) to[row] = x[0];
 }
 
-// 16 bytes of the cache into shared memory, asynchronously.
-__device__ inline void copy16(void *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+// 16 bytes of the cache into shared memory, asynchronously; zeros where there are none.
+__device__ inline void copy16(void *dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 __device__ inline void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All of the thread's copies but those of the last N groups have arrived.
@@ -228,52 +237,47 @@ __device__ inline void copies_wait() { asm volatile("cp.async.wait_group %0;" ::
 template <int D, int R>
 __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kPerSm) kv4_decode_kernel(Attn p) {
     using Cfg = DecodeCfg<D, R>;
-    constexpr int W = Cfg::kGroups;
     extern __shared__ __align__(1024) uint8_t s_dyn[];
-    uint8_t *const sQ = s_dyn, *const s_groups = sQ + Cfg::kQ;
+    uint8_t *const sQ = s_dyn, *const sV = sQ + Cfg::kQ, *const sP = sV + Cfg::kV;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint8_t *const k_raw = sP + Cfg::kPs * Cfg::kP + warp * Cfg::kWarpRaw, *const v_raw = k_raw + Cfg::kRaw;
+    DecodeShared<R> &sh = *reinterpret_cast<DecodeShared<R> *>(s_dyn + Cfg::kSmem);
     // the sequences' prefix: needed only before the first operand is written
-    int *const s_pre = reinterpret_cast<int *>(s_groups);
-    static_assert(sizeof(int) * 4097 <= (size_t)W * Cfg::kGroup, "prefix");
-    DecodeShared<W, R> &sh = *reinterpret_cast<DecodeShared<W, R> *>(s_groups + W * Cfg::kGroup);
-    Bars &bars = sh.bars;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2, tid = threadIdx.x & 127;
-    const int bar = 1 + wg;   // the warpgroup's barrier
+    int *const s_pre = reinterpret_cast<int *>(sV);
+    static_assert(sizeof(int) * 4097 <= (size_t)(Cfg::kV + Cfg::kPs * Cfg::kP), "prefix");
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < W; ++i) {
-            mbar_init(&bars.s_full[i], 1);
-            mbar_init(&bars.o_full[i], 1);
-            sh.fail[i] = 0;
-        }
+    if (tid == 0) {
+        mbar_init(&sh.s_full, 1);
+        mbar_init(&sh.o_full, 1);
         fence_mbar_init();
     }
-    uint8_t *const sV = s_groups + wg * Cfg::kGroup, *const sP = sV + Cfg::kV;
-    uint8_t *const k_raw = sP + Cfg::kPs * Cfg::kP + (warp & 3) * Cfg::kWarpRaw, *const v_raw = k_raw + Cfg::kRaw;
     pdl_wait();
     pdl_launch_dependents();
-    const int U = scan_units<Cfg::kThreads, kKeys>(p, R, s_pre, sh.sums);
-    // fewer CTAs where there is less than a unit for each warpgroup of them
-    const Shares shares(U, min((int)gridDim.x, max(1, (U + W - 1) / W)));
-    const int c = blockIdx.x;
-    if (c >= shares.C || U == 0) return;
-    int u = shares.begin(c);
-    const int u_end = shares.begin(c + 1);
-    if (warp == 0) {
-        tc::alloc(&sh.tmem, W * Cfg::kCols);
+    if (warp == 0) {   // (only now: the kernel ahead may hold tensor memory that it has not freed)
+        tc::alloc(&sh.tmem, Cfg::kCols);
         tc::relinquish();
     }
+    const int c = blockIdx.x;
+    Item it;
+    const Shares shares = first_item<Cfg::kThreads, kKeys>(p, R, c, s_pre, sh.sums, sh.first, it);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    const uint32_t tcol = sh.tmem + wg * Cfg::kCols, tlane = tcol + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t tcol = sh.tmem, tlane = tcol + ((uint32_t)(warp * 32) << 16);
+    if (c >= shares.C) {
+        if (tid == 0) p.begun[c].last = 0;
+        if (warp == 0) tc::dealloc(tcol, Cfg::kCols);
+        return;
+    }
+    int u = shares.begin(c);
+    const int u_end = shares.begin(c + 1);
     uint32_t n_s = 0, n_o = 0;   // products of scores and of values waited for
 
     // ---- a unit's place in the cache. A warp's 32 keys are two runs of 16, each in one
     // page (page sizes are multiples of 16): lane i knows the run of keys 16 (i / 16) ...
     constexpr uint32_t kNone = 0xffffffffu;   // no such keys, or a page that does not exist: they read as zero
-    Item it = find_item<kKeys>(p, R, s_pre, u);
     int st0 = u - it.first, st1 = min(it.units, u_end - it.first);   // the units of the item in this CTA's share
-    const int run = (warp & 3) * 32 + (lane & 16);
+    const int run = warp * 32 + (lane & 16);
     auto page_of = [&](int st) {
         const int key = st * kKeys + run;
         return st < st1 && key < it.s.len ? ld_here(p.b.table + (size_t)it.b * p.b.max_pages + (key >> p.b.shift)) : -1;
@@ -289,26 +293,28 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
     };
     // The warp's rows, 512 bytes at a time. The 16-byte pieces of a row are turned by the
     // row, so that lanes that read a row each meet no bank twice. Rows that do not exist
-    // keep what was there (codes are finite whatever they are).
+    // become zeros.
     auto turned = [](int r) { return D == 128 ? r >> 1 & 3 : r >> 2 & 1; };
     const int copy_to = (lane / Cfg::kChunks * Cfg::kChunks + (lane % Cfg::kChunks ^ turned(lane / Cfg::kChunks))) * 16;
-    auto copy = [&](uint8_t *raw, const int32_t *codes, uint32_t at) {
+    const char *const k_from = reinterpret_cast<const char *>(p.c.k_codes) + lane * 16, *const v_from = reinterpret_cast<const char *>(p.c.v_codes) + lane * 16;
+    struct Runs {
+        uint32_t a, b;   // first rows of the warp's two runs
+    };
+    auto runs_of = [&](uint32_t at) { return Runs{__shfl_sync(0xffffffffu, at, 0), __shfl_sync(0xffffffffu, at, 16)}; };
+    auto copy = [&](uint8_t *raw, const char *from, Runs runs) {
+        const bool is_a = runs.a != kNone, is_b = runs.b != kNone;
+        const char *fa = from + (size_t)(is_a ? runs.a : 0) * (D / 2), *fb = from + (size_t)(is_b ? runs.b : 0) * (D / 2);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t src = __shfl_sync(0xffffffffu, at, 16 * i);
-            if (src != kNone) {
-                const char *from = reinterpret_cast<const char *>(codes) + (size_t)src * (D / 2) + lane * 16;
-                uint8_t *to = raw + i * (8 * D) + copy_to;
-#pragma unroll
-                for (int k = 0; k < D / 64; ++k) copy16(to + k * 512, from + k * 512);
-            }
+        for (int k = 0; k < D / 64; ++k) {
+            copy16(raw + copy_to + k * 512, fa + k * 512, is_a);
+            copy16(raw + copy_to + 8 * D + k * 512, fb + k * 512, is_b);
         }
     };
     // the scales: a run's are 32 bytes; lanes 0-1 and 16-17 copy K's, 2-3 and 18-19 V's
+    const uint16_t *const scales_from = ((lane & 2) ? p.c.v_scales : p.c.k_scales) + (lane & 1) * 8;
+    uint16_t *const scales_to = &sh.scales[warp][0][lane >> 1 & 1][(lane & 16) + (lane & 1) * 8];
     auto copy_scales = [&](int slot, uint32_t at) {
-        if ((lane & 15) < 4 && at != kNone)
-            copy16(&sh.scales[warp][slot][lane >> 1 & 1][(lane & 16) + (lane & 1) * 8],
-                   ((lane & 2) ? p.c.v_scales : p.c.k_scales) + at + (lane & 1) * 8);
+        if ((lane & 15) < 4) copy16(scales_to + slot * 64, scales_from + (at != kNone ? at : 0), at != kNone);
     };
     auto row_of = [&](const uint8_t *raw, uint4 (&w)[Cfg::kChunks]) {
 #pragma unroll
@@ -339,49 +345,55 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
             }
         }
     };
+    const uint64_t desc_q = tc::sdesc_sw128(sQ), desc_v = v_desc<D>(sV), desc_p = p_desc<R>(sP);
     auto issue_scores = [&]() {
-        if ((warp & 3) == 0 && elect()) {
+        if (elect()) {   // (warp 0)
 #pragma unroll
             for (int k = 0; k < D / 32; ++k)
-                mma_e4m3(tcol + Cfg::kColS, tcol + k * 8, tc::sdesc_sw128(sQ) + (uint64_t)(k * 2), idesc(Cfg::kNS, false), k > 0);
-            tc::commit(&bars.s_full[wg]);
+                mma_e4m3(tcol + Cfg::kColS, tcol + k * 8, desc_q + (uint64_t)(k * 2), idesc(Cfg::kNS, false), k > 0);
+            tc::commit(&sh.s_full);
         }
         __syncwarp();
     };
-    // The first copies of an item: K and scales of the warpgroup's first unit, and V's (in
-    // no group yet). They are begun before what else the item's start or the last one's
+    // The first copies of an item (K and scales of its first unit, and V's, in no group
+    // yet) and its queries are begun before what else the item's start or the last one's
     // end has to do.
-    int page0 = page_of(st0 + wg), page1 = page_of(st0 + wg + W);
-    uint32_t at0 = kNone;   // the runs of this unit, of the next (whose K is under way)
-    auto begin_copies = [&]() {
-        at0 = place(st0 + wg, page0);
-        copy(k_raw, p.c.k_codes, at0);
+    int page0 = page_of(st0), page1 = page_of(st0 + 1), rows;
+    uint32_t at0 = kNone, at1 = kNone;   // where this unit and the next (whose K is under way) lie
+    uint2 q_raw[R / 4];                  // the warp's rows r = warp + 4 i, D / 32 values a lane
+    auto begin_item = [&]() {
+        rows = min(R, it.s.nq * p.G - it.qt * R);
+#pragma unroll
+        for (int i = 0; i < R / 4; ++i) {
+            const int r = warp + 4 * i, rr = it.qt * R + r, qi = rr / p.G;
+            q_raw[i] = make_uint2(0, 0);
+            if (r < rows) {
+                const uint16_t *src = p.q + (size_t)(it.s.q0 + qi) * p.qs.token + (size_t)(it.h * p.G + rr - qi * p.G) * p.qs.head + lane * (D / 32);
+                if (D == 128) q_raw[i] = *reinterpret_cast<const uint2 *>(src);
+                else q_raw[i].x = *reinterpret_cast<const uint32_t *>(src);
+            }
+        }
+        at0 = place(st0, page0);
+        copy(k_raw, k_from, runs_of(at0));
         copy_scales(0, at0);
         copies_commit();
-        copy(v_raw, p.c.v_codes, at0);
+        copy(v_raw, v_from, runs_of(at0));
     };
-    begin_copies();
+    begin_item();
 
     for (;;) {
-        const int rows = min(R, it.s.nq * p.G - it.qt * R);
-
         // ---- the rows' queries as operands, and what each row sees
-        for (int r = warp; r < R; r += 4 * W) {
-            const int rr = it.qt * R + r, i = rr / p.G;
+#pragma unroll
+        for (int i = 0; i < R / 4; ++i) {
+            const int r = warp + 4 * i, qi = (it.qt * R + r) / p.G;
+            const uint32_t v[2] = {q_raw[i].x, q_raw[i].y};
             float x[D / 32];
             uint32_t big = 0;
-            if (r < rows) {
-                const uint16_t *src = p.q + (size_t)(it.s.q0 + i) * p.qs.token + (size_t)(it.h * p.G + rr - i * p.G) * p.qs.head + lane * (D / 32);
 #pragma unroll
-                for (int j = 0; j < D / 32; j += 2) {
-                    const uint32_t v = *reinterpret_cast<const uint32_t *>(src + j);
-                    x[j] = __uint_as_float(v << 16);
-                    x[j + 1] = __uint_as_float(v & 0xffff0000u);
-                    big = max(big, max(v & 0x7FFFu, (v >> 16) & 0x7FFFu));
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < D / 32; ++j) x[j] = 0.f;
+            for (int j = 0; j < D / 32; j += 2) {
+                x[j] = __uint_as_float(v[j / 2] << 16);
+                x[j + 1] = __uint_as_float(v[j / 2] & 0xffff0000u);
+                big = max(big, max(v[j / 2] & 0x7FFFu, (v[j / 2] >> 16) & 0x7FFFu));
             }
             big = __reduce_max_sync(0xffffffffu, big);
             const int e = norm_exponent(big);
@@ -409,12 +421,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
                 const float cc = fmaxf(fabsf(p.scale) * kLog2e * pow2_biased(e) * 4.f, 1e-37f);
                 sh.c[r] = big < 0x7F80u ? cc : __uint_as_float(0x7fc00000u);   // a query that is not finite: NaN
                 sh.base[r] = sum * (-8.f / 512.f);
-                sh.lim[r] = r < rows ? it.s.len - it.s.nq + i + 1 : 0;
+                sh.lim[r] = r < rows ? it.s.len - it.s.nq + qi + 1 : 0;
             }
         }
-        if (tid < R) sh.m[wg][tid] = 0.f;   // (the first unit sets it)
         fence_proxy_async_smem();
         __syncthreads();
+        if (tid < R) sh.m[tid] = 0.f;   // (the first unit sets it)
         // every row sees the keys below `least`
         const int least = max(it.s.len - it.s.nq + it.qt * R / p.G + 1, 0);
 
@@ -423,29 +435,26 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
         for (int r = 0; r < R; ++r) l[r] = 0.f;
         int F = 1;            // biased exponent taken off the V scales
         float v_top = 0.f;    // 2^(F - 126): they stay below it (0: the first unit takes the branch that sets both)
-        int st = st0 + wg, slot = 0;   // slot: of this unit's scales
-        const bool any = st < st1;     // (uniform in a warpgroup)
-        uint32_t at1 = kNone;
-        bool cut = false;     // a wait gave up
-        if (any) {
-            copies_wait<0>();   // (K; V belongs to the next group)
-            __syncwarp();
-            write_k();
-            __syncwarp();
-            at1 = place(st + W, page1);
-            page1 = page_of(st + 2 * W);
-            copy(k_raw, p.c.k_codes, at1);
-            copy_scales(1, at1);
-            copies_commit();
-            copies_commit();   // (in each turn K's group is the last but one where it is waited for)
-            tc::wait_st();
-            tc::fence_before();
-            bar_sync(bar);
-            tc::fence_after();
-            issue_scores();
-        }
-        for (uint32_t turn = 0; st < st1; st += W, ++turn) {
-            const bool more = st + W < st1;
+        int st = st0, slot = 0;   // slot: of this unit's scales
+        bool fail = false;        // a wait gave up
+        copies_wait<0>();   // (K; V belongs to the next group)
+        __syncwarp();
+        write_k();
+        __syncwarp();
+        at1 = place(st + 1, page1);
+        page1 = page_of(st + 2);
+        Runs runs = runs_of(at1);   // of the next unit
+        copy(k_raw, k_from, runs);
+        copy_scales(1, at1);
+        copies_commit();
+        copies_commit();   // (in each turn K's group is the last but one where it is waited for)
+        tc::wait_st();
+        tc::fence_before();
+        __syncthreads();
+        tc::fence_after();
+        if (warp == 0) issue_scores();
+        for (uint32_t turn = 0; st < st1; ++st, ++turn) {
+            const bool more = st + 1 < st1;
             // ---- the key's scores, less the maxima in use. Scales: a row that was not finite
             // makes its scores NaN, its values zero
             const int key = st * kKeys + tid;
@@ -456,7 +465,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
                 fk = __uint_as_float(0x7fc00000u);
                 fv = 0.f;
             }
-            bool fail = !wait(&bars.s_full[wg], n_s & 1);
+            fail |= !wait(&sh.s_full, n_s & 1);
             ++n_s;
             tc::fence_after();
             float s[R];
@@ -466,7 +475,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
 #pragma unroll
                 for (int r = 0; r < R; r += 4) {
                     const float4 base = *reinterpret_cast<const float4 *>(sh.base + r), cs = *reinterpret_cast<const float4 *>(sh.c + r),
-                                 m = *reinterpret_cast<const float4 *>(sh.m[wg] + r);
+                                 m = *reinterpret_cast<const float4 *>(sh.m + r);
                     float *x = s2 + r, *y = s2 + R + r;
                     add2(x[0], x[1], y[0], y[1]);
                     add2(x[2], x[3], y[2], y[3]);
@@ -483,15 +492,24 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
             // ---- the next unit's K, whose product runs beside what follows
             slot = slot == 2 ? 0 : slot + 1;
             at0 = at1;
+            Runs runs_next{kNone, kNone};
             if (more) {
                 copies_wait<1>();
                 __syncwarp();
                 write_k();
                 __syncwarp();
-                at1 = place(st + 2 * W, page1);
-                page1 = page_of(st + 3 * W);
-                copy(k_raw, p.c.k_codes, at1);
+                at1 = place(st + 2, page1);
+                page1 = page_of(st + 3);
+                runs_next = runs_of(at1);
+                copy(k_raw, k_from, runs_next);
                 copy_scales(slot == 2 ? 0 : slot + 1, at1);
+                tc::wait_st();
+                tc::fence_before();
+                bar_pass(warp);
+                if (warp == 0) {
+                    tc::fence_after();
+                    issue_scores();
+                }
             }
             copies_commit();
             if ((st + 1) * kKeys > least) {
@@ -499,43 +517,71 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
                 for (int r = 0; r < R; ++r)
                     if (key >= sh.lim[r]) s[r] = -INFINITY;
             }
-            bool over = fabsf(fv) >= v_top;
+            bool over = !(fabsf(fv) < v_top);
 #pragma unroll
             for (int r = 0; r < R; ++r) over |= s[r] > 8.f;
-            tc::wait_st();
-            tc::fence_before();
-            const bool move = bar_or(bar, over);
-            tc::fence_after();
-            if (more) issue_scores();
-            bool added = turn == 0;   // the last unit's values are in the sums
-            if (move) {
-                // ---- a score passed the maximum in use by 2^8, or a V scale its exponent: all follow
-                reduce_rows<R, true>(s, sh.wm[wg][warp & 3]);
-                const uint32_t e = __reduce_max_sync(0xffffffffu, __float_as_uint(fv) >> 23 & 0xFFu);
-                if (lane == 0) sh.we[wg][warp & 3] = (int)e;
-                bar_sync(bar);
-                int Fn = F;
+            // ---- probabilities; where a score passed the maximum in use by 2^8, or a V scale its
+            // exponent, the warp leaves them until all have followed
+            over = __any_sync(0xffffffffu, over);
+            const uint32_t p_at = Cfg::kPs == 2 ? (turn & 1) * Cfg::kP : 0;
+            auto values_added = [&]() {   // the last unit's values are in the sums, and V and P free
+                if (turn > 0) {
+                    fail |= !wait(&sh.o_full, n_o & 1);
+                    ++n_o;
+                }
+            };
+            auto write_p = [&](bool sum) {
+                const float f = fv * pow2_biased(254 - F);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) Fn = max(Fn, min(sh.we[wg][i], 253));
+                for (int r = 0; r < R; r += 8) {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) {
+                        float a = exp2_approx(s[r + j]), b = exp2_approx(s[r + j + 1]);
+                        if (sum) add2(l[r + j], l[r + j + 1], a, b);
+                        mul2(a, b, f, f);
+                        h[j >> 1] = half2_of(a, b);
+                    }
+                    *reinterpret_cast<uint4 *>(sP + p_at + tid * 16 + (r >> 3) * 2048) = make_uint4(h[0], h[1], h[2], h[3]);
+                }
+            };
+            if (Cfg::kPs == 1) values_added();
+            if (!over) write_p(true);
+            // ---- the unit's V
+            if (Cfg::kPs == 2) values_added();
+            copies_wait<1>();
+            __syncwarp();
+            write_v();
+            __syncwarp();
+            if (more) copy(v_raw, v_from, runs);
+            runs = runs_next;
+            copies_commit();
+            fence_proxy_async_smem();
+            tc::fence_before();
+            if (bar_or(over || fail)) {
+                tc::fence_after();
+                if (bar_or(fail)) break;   // a wait gave up: for all warps at once
+                // ---- all follow: the maxima, the exponent, the sums
+                reduce_rows<R, true>(s, sh.wm[warp]);
+                const uint32_t e = __reduce_max_sync(0xffffffffu, __float_as_uint(fv) >> 23 & 0xFFu);
+                if (lane == 0) sh.we[warp] = (int)e;
+                __syncthreads();
+                const int Fn = max(F, min(max(max(sh.we[0], sh.we[1]), max(sh.we[2], sh.we[3])), 253));
                 const float fo = Fn - F > 126 ? 0.f : pow2_biased(127 + F - Fn);
                 F = Fn;
                 v_top = F == 253 ? INFINITY : pow2_biased(F + 1);
                 float up[R];   // how far each row's maximum rises, then 2 to less that
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const float x = fmaxf(fmaxf(sh.wm[wg][0][r], sh.wm[wg][1][r]), fmaxf(sh.wm[wg][2][r], sh.wm[wg][3][r]));
+                    const float x = fmaxf(fmaxf(sh.wm[0][r], sh.wm[1][r]), fmaxf(sh.wm[2][r], sh.wm[3][r]));
                     // (a row that sees no key of the first unit sees none of the later ones)
                     up[r] = turn > 0 ? fmaxf(x, 0.f) : x == kNoMax ? 0.f : x;
-                    if (tid == r) sh.m[wg][r] += up[r];   // (all have read the old maxima before the first barrier)
+                    if (tid == r) sh.m[r] += up[r];   // (all have read the old maxima before the barriers)
                     s[r] -= up[r];
                     up[r] = exp2_approx(-up[r]);
                     l[r] *= up[r];
                 }
                 if (turn > 0) {
-                    fail |= !wait(&bars.o_full[wg], n_o & 1);
-                    ++n_o;
-                    added = true;
-                    tc::fence_after();
                     float o[R];
                     ld_cols<R>(tlane + Cfg::kColO, o);
                     uint32_t w[R];
@@ -544,184 +590,119 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
                     st_cols<R>(tlane + Cfg::kColO, w);
                     tc::wait_st();
                 }
-            }
-            // ---- probabilities
-            fv *= pow2_biased(254 - F);
-            uint8_t *const sPn = sP + (Cfg::kPs == 2 ? (turn & 1) * Cfg::kP : 0);
-            auto values_added = [&]() {   // the last unit's values are in the sums, and V and P free
-                if (!added) {
-                    fail |= !wait(&bars.o_full[wg], n_o & 1);
-                    ++n_o;
-                }
-            };
-            if (Cfg::kPs == 1) values_added();
-#pragma unroll
-            for (int r = 0; r < R; r += 8) {
-                uint32_t h[4];
-#pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    float a = exp2_approx(s[r + j]), b = exp2_approx(s[r + j + 1]);
-                    add2(l[r + j], l[r + j + 1], a, b);
-                    mul2(a, b, fv, fv);
-                    h[j >> 1] = half2_of(a, b);
-                }
-                *reinterpret_cast<uint4 *>(sPn + (r >> 3) * 2048 + tid * 16) = make_uint4(h[0], h[1], h[2], h[3]);
-            }
-            // ---- the unit's V
-            if (Cfg::kPs == 2) values_added();
-            copies_wait<1>();
-            __syncwarp();
-            write_v();
-            __syncwarp();
-            if (more) copy(v_raw, p.c.v_codes, at0);
-            copies_commit();
-            fence_proxy_async_smem();
-            tc::fence_before();
-            // a wait that gave up ends the warpgroup's turns here, for all its warps at once
-            if (bar_or(bar, fail)) {
-                sh.fail[wg] = 1;
-                cut = true;
-                break;
+                if (over) write_p(true);
+                else write_p(false);   // (its sums hold them already)
+                fence_proxy_async_smem();
+                tc::fence_before();
+                __syncthreads();
             }
             tc::fence_after();
-            if ((warp & 3) == 0 && elect()) {
+            if (warp == 1 && elect()) {
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k)
-                    tc::mma_ss(tcol + Cfg::kColO, v_desc<D>(sV) + (uint64_t)(k * 128), p_desc<R>(sPn) + (uint64_t)(k * 16),
-                               idesc(Cfg::kNP, true), turn > 0 || k > 0);
-                tc::commit(&bars.o_full[wg]);
+                    tc::mma_ss(tcol + Cfg::kColO, desc_v + (uint64_t)(k * 128), desc_p + (uint64_t)(p_at / 16 + k * 16), idesc(Cfg::kNP, true),
+                               turn > 0 || k > 0);
+                tc::commit(&sh.o_full);
             }
             __syncwarp();
         }
+        copies_wait<0>();
+        if (st < st1) {   // (cut short; the products in flight get a bounded wait)
+            wait(&sh.o_full, n_o & 1);
+            if (tid == 0) {
+                set_error(p.ctrl, MOE_ERR_TIMEOUT);
+                p.begun[c].last = 0;
+            }
+            break;
+        }
 
-        // ---- the next item's pages
+        // ---- the next item's first copies, then this one's rows
         const Item done = it;
-        const bool whole = st0 == 0 && st1 == it.units, first_part = st0 == 0;
+        const bool first_part = st0 == 0, whole = first_part && st1 == it.units;
         u = it.first + st1;
         const bool last_item = u >= u_end;
         if (!last_item) {
             next_item<kKeys>(p, R, it);
             st0 = 0;
             st1 = min(it.units, u_end - u);
-            page0 = page_of(wg);
-            page1 = page_of(wg + W);
+            page0 = page_of(0);
+            page1 = page_of(1);
         }
-        // ---- the warpgroups' rows, side by side in shared memory (where V was)
-        if (any && !cut) {
-            if (!wait(&bars.o_full[wg], n_o & 1)) sh.fail[wg] = 1;
-            ++n_o;
-            tc::fence_after();
-        }
-        float *const s_o = reinterpret_cast<float *>(sV);
-        {
-            float o[R];
-            if (any) ld_cols<R>(tlane + Cfg::kColO, o);
-            else
-#pragma unroll
-                for (int r = 0; r < R; ++r) o[r] = 0.f;
-            // lane x holds place x of the values' order 0, 4, 1, 5, 2, 6, 3, 7
-            const int d = (tid & ~7) + ((tid & 7) >> 1) + (tid & 1) * 4;
-            if (tid < D)
-#pragma unroll
-                for (int r = 0; r < R; ++r) s_o[r * Cfg::kStride + d] = o[r];
-        }
-        reduce_rows<R, false>(l, sh.wm[wg][warp & 3]);
-        if (tid == 0) sh.F[wg] = F;
-        copies_wait<0>();
-        if (!last_item) begin_copies();
-        tc::fence_before();
-        __syncthreads();
+        reduce_rows<R, false>(l, sh.wm[warp]);
+        fail = !wait(&sh.o_full, n_o & 1);
+        ++n_o;
         tc::fence_after();
-        bool failed = false;
-#pragma unroll
-        for (int w = 0; w < W; ++w) failed |= sh.fail[w] != 0;
-        if (failed) {
-            if (threadIdx.x == 0) set_error(p.ctrl, MOE_ERR_TIMEOUT);
+        float o[R];
+        ld_cols<R>(tlane + Cfg::kColO, o);
+        const int rows_done = rows;
+        if (!last_item) begin_item();
+        tc::fence_before();
+        if (bar_or(fail)) {
+            if (tid == 0) {
+                set_error(p.ctrl, MOE_ERR_TIMEOUT);
+                p.begun[c].last = 0;
+            }
             break;
         }
-        if (tid < R) {
-            const float sum = (sh.wm[wg][0][tid] + sh.wm[wg][1][tid]) + (sh.wm[wg][2][tid] + sh.wm[wg][3][tid]);
-            sh.l[wg][tid] = sum;
-            if (sum == 0.f) sh.m[wg][tid] = kNoMax;   // nothing seen
-        }
-        __syncthreads();
-        int Fm = 1;
-#pragma unroll
-        for (int w = 0; w < W; ++w) Fm = max(Fm, sh.F[w]);
-        // a CTA's first part continues an item, its last one may begin one
+        // lane x holds place x of the values' order 0, 4, 1, 5, 2, 6, 3, 7
+        const int d = (tid & ~7) + ((tid & 7) >> 1) + (tid & 1) * 4;
         float *part = p.part + (size_t)(c * 2 + first_part) * part_floats(R, D);
-        for (int x = threadIdx.x; x < rows * (D / 4); x += Cfg::kThreads) {
-            const int r = x / (D / 4), d = (x % (D / 4)) * 4;
-            float M = kNoMax, L = 0.f;
+        const float up = pow2_biased(F);
 #pragma unroll
-            for (int w = 0; w < W; ++w) M = fmaxf(M, sh.m[w][r]);
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const float f = exp2_approx(sh.m[w][r] - M);
-                L = fmaf(sh.l[w][r], f, L);
-                const float fv = Fm - sh.F[w] > 126 ? 0.f : f * pow2_biased(127 + sh.F[w] - Fm);
-                const float4 v = *reinterpret_cast<const float4 *>(s_groups + w * Cfg::kGroup + (r * Cfg::kStride + d) * 4);
-                acc.x = fmaf(v.x, fv, acc.x);
-                acc.y = fmaf(v.y, fv, acc.y);
-                acc.z = fmaf(v.z, fv, acc.z);
-                acc.w = fmaf(v.w, fv, acc.w);
-            }
+        for (int r = 0; r < R; ++r) {
+            if (r >= rows_done) break;
+            const float sum = (sh.wm[0][r] + sh.wm[1][r]) + (sh.wm[2][r] + sh.wm[3][r]);
             if (whole) {
-                write_row4(p, done, R, r, d, acc, M, L, Fm);
+                const int rr = done.qt * R + r, i = rr / p.G, head = done.h * p.G + rr - i * p.G;
+                const size_t tok = (size_t)(done.s.q0 + i);
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;   // (no key: zero)
+                const __nv_bfloat16 x = __float2bfloat16_rn(o[r] * inv * up);
+                if (tid < D) p.out[tok * p.os.token + (size_t)head * p.os.head + d] = *reinterpret_cast<const uint16_t *>(&x);
+                if (tid == r && p.lse) p.lse[tok * p.Hq + head] = sum == 0.f ? -INFINITY : (sh.m[r] + log2f(sum)) * kLn2;
             } else {
-                *reinterpret_cast<float4 *>(part + 2 * R + 4 + r * D + d) = acc;
-                if (d == 0) {
-                    part[r] = M;
-                    part[R + r] = L;
+                if (tid < D) part[2 * R + 4 + r * D + d] = o[r];
+                if (tid == r) {
+                    part[r] = sum == 0.f ? kNoMax : sh.m[r];   // (nothing seen)
+                    part[R + r] = sum;
                 }
-                if (x == 0) part[2 * R] = __int_as_float(Fm);
             }
         }
-        __syncthreads();   // (also: the item's shared memory is free)
-        if (!whole) {
-            const int c0 = shares.holder(done.first), c1 = shares.holder(done.first + done.units - 1);
-            if (threadIdx.x == 0) {
-                __threadfence();
-                const uint32_t n = atom_acq_rel_add_u32(p.ticket + c0, 1u);
-                sh.last = n == (uint32_t)(c1 - c0);
-                if (sh.last) p.ticket[c0] = 0;
-            }
-            __syncthreads();
-            if (sh.last) {
-                __threadfence();
-                join_parts<Cfg::kThreads, R, D>(p, done, rows, c0, c1);
-            }
-            __syncthreads();
+        if (tid == 0) {
+            if (!whole) part[2 * R] = __int_as_float(F);
+            if (last_item)
+                p.begun[c] = Begun{first_part && !whole ? shares.holder(done.first + done.units - 1) : 0, done.s.q0, done.h, done.qt, rows_done, {0, 0, 0}};
         }
         if (last_item) break;
     }
     copies_wait<0>();
-    // (after a wait that gave up, the products still in flight get another bounded one)
-    if (sh.fail[wg]) wait(&bars.o_full[wg], n_o & 1);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    if (warp == 0) tc::dealloc(sh.tmem, W * Cfg::kCols);
+    if (warp == 0) tc::dealloc(sh.tmem, Cfg::kCols);
 }
 
 template <int D, int R>
-cudaError_t launch_one(const Attn &p, cudaStream_t s) {
+cudaError_t launch_one(const Attn &p, int *rows_at, int *grid_out, cudaStream_t s) {
     using Cfg = DecodeCfg<D, R>;
-    constexpr size_t kBase = Cfg::kSmem + sizeof(DecodeShared<Cfg::kGroups, R>);
-    static_assert(kBase <= (size_t)(Cfg::kPerSm == 2 ? 115712 : 231424), "shared memory");
-    const cudaError_t err = set_smem_once(reinterpret_cast<const void *>(kv4_decode_kernel<D, R>), (int)kBase);
+    constexpr size_t kBytes = Cfg::kSmem + sizeof(DecodeShared<R>);
+    static_assert((kBytes + 1024) * Cfg::kPerSm <= 233472, "shared memory");
+    const cudaError_t err = set_smem_once(reinterpret_cast<const void *>(kv4_decode_kernel<D, R>), (int)kBytes);
     if (err != cudaSuccess) return err;
     int grid = Cfg::kPerSm * sm_count();
     if (grid > kMaxCtas) grid = kMaxCtas;
-    return launch_pdl(kv4_decode_kernel<D, R>, dim3((unsigned)grid), Cfg::kThreads, kBase, s, p);
+    *rows_at = R;
+    *grid_out = grid;
+    return launch_pdl(kv4_decode_kernel<D, R>, dim3((unsigned)grid), Cfg::kThreads, kBytes, s, p);
 }
 
 }  // namespace
 
-cudaError_t launch_kv4_decode(const kv4::Attn &p, int rows, cudaStream_t s) {
-    if (p.c.D == 64) return rows <= 8 ? launch_one<64, 8>(p, s) : rows <= 16 ? launch_one<64, 16>(p, s) : launch_one<64, 32>(p, s);
-    return rows <= 8 ? launch_one<128, 8>(p, s) : rows <= 16 ? launch_one<128, 16>(p, s) : launch_one<128, 32>(p, s);
+cudaError_t launch_kv4_decode(const kv4::Attn &p, int rows, int *rows_at, int *grid, cudaStream_t s) {
+    auto pick = [&](auto d) {
+        constexpr int D = decltype(d)::value;
+        return rows <= 8 ? launch_one<D, 8>(p, rows_at, grid, s) : rows <= 16 ? launch_one<D, 16>(p, rows_at, grid, s) : launch_one<D, 32>(p, rows_at, grid, s);
+    };
+    return p.c.D == 64 ? pick(std::integral_constant<int, 64>{}) : pick(std::integral_constant<int, 128>{});
 }
 
 }  // namespace moe

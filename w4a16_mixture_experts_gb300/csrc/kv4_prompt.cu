@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
     __shared__ Bars bars;
     __shared__ long long s_sums[kThreads / 32];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort, s_last;
+    __shared__ int s_abort;
     __shared__ int s_E[4], s_F[4], s_red[2][2][4];   // a stage's K exponent, V exponent so far (rings of 4 stages)
     volatile int *const abort_flag = &s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -199,7 +199,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
     const int U = scan_units<kThreads, kKeys>(p, kR, s_pre, s_sums);
     const Shares shares(U, min((int)gridDim.x, max(1, U)));
     const int c = blockIdx.x;
-    if (c >= shares.C || U == 0) return;   // (the whole CTA)
+    if (c >= shares.C || U == 0) {   // (the whole CTA)
+        if (threadIdx.x == 0) p.begun[c].last = 0;
+        return;
+    }
     const int u_begin = shares.begin(c), u_end = shares.begin(c + 1);
     if (warp == kWMma) {
         tc::alloc(&s_tmem, 512);
@@ -368,22 +371,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                 }
             }
             tc::fence_before();
-            if (!whole) {
-                ok = bar_and(1, 256, ok);
-                const int c0 = shares.holder(it.first), c1 = shares.holder(it.first + it.units - 1);
-                if (ok && threadIdx.x == 0) {
-                    __threadfence();
-                    const uint32_t n = atom_acq_rel_add_u32(p.ticket + c0, 1u);
-                    s_last = n == (uint32_t)(c1 - c0);
-                    if (s_last) p.ticket[c0] = 0;
-                }
-                ok = bar_and(1, 256, ok);
-                if (ok && s_last) {
-                    __threadfence();
-                    join_parts<256, kR, D>(p, it, rows, c0, c1);
-                }
-            }
             u = it.first + st1;
+            if (threadIdx.x == 0 && (!ok || u >= u_end)) {
+                const bool goes_on = ok && st0 == 0 && !whole;
+                p.begun[c] = Begun{goes_on ? shares.holder(it.first + it.units - 1) : 0, it.s.q0, it.h, it.qt, rows, {0, 0, 0}};
+            }
             if (!ok) {
                 *abort_flag = 1;
                 if (lane == 0) set_error(p.ctrl, MOE_ERR_TIMEOUT);
@@ -577,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
 }
 
 template <int D>
-cudaError_t launch_one(const Attn &p, cudaStream_t s) {
+cudaError_t launch_one(const Attn &p, int *grid_out, cudaStream_t s) {
     const void *fn = reinterpret_cast<const void *>(kv4_prompt_kernel<D>);
     // The register split takes what the launch reserves: it must be the whole of it.
     static const bool split_ok = [fn] {
@@ -590,13 +582,14 @@ cudaError_t launch_one(const Attn &p, cudaStream_t s) {
     if (err != cudaSuccess) return err;
     int grid = sm_count();
     if (grid > kMaxPromptCtas) grid = kMaxPromptCtas;
+    *grid_out = grid;
     return launch_pdl(kv4_prompt_kernel<D>, dim3((unsigned)grid), kThreads, kBase + sizeof(int) * ((size_t)p.b.B + 1), s, p);
 }
 
 }  // namespace
 
-cudaError_t launch_kv4_prompt(const kv4::Attn &p, cudaStream_t s) {
-    return p.c.D == 64 ? launch_one<64>(p, s) : launch_one<128>(p, s);
+cudaError_t launch_kv4_prompt(const kv4::Attn &p, int *grid, cudaStream_t s) {
+    return p.c.D == 64 ? launch_one<64>(p, grid, s) : launch_one<128>(p, grid, s);
 }
 
 }  // namespace moe
