@@ -3,9 +3,11 @@
 //
 // An item is up to R query rows of one (sequence, KV head); row r of a sequence
 // is query r / G, head r % G of the group. Its work is a number of units, each a
-// fixed count of keys. All items' units lie one after another and CTA c of C
-// takes the units [U c / C, U (c + 1) / C), whatever items they belong to: an
-// even share for any mix of lengths. The parts of an item that lies in several
+// fixed count of keys, and what beginning and ending it costs, as kLead units
+// before those. All items' units lie one after another and CTA c of C takes the
+// units [U c / C, U (c + 1) / C), whatever items they belong to: an even share
+// for any mix of lengths. (A border among an item's leading units is one before
+// it.) The parts of an item that lies in several
 // CTAs' shares are joined, in the CTAs' order, by a second kernel, which the
 // whole card runs. (The last of the CTAs to finish joining them alone took up to
 // 60 us of a prompt chunk's 180, and its fence and ticket 1 us of the others.)
@@ -116,61 +118,32 @@ __device__ inline int tile_keys(const Seq &s, int G, int R, int qt) {
     return min(max(s.len - s.nq + last + 1, 0), s.len);
 }
 
-// Units of a sequence's row tile: at least one, so that rows that see no key
-// are written too.
+// Units of keys of a sequence's row tile: at least one, so that rows that see no
+// key are written too.
 template <int kKeys>
 __device__ inline int tile_units(const Seq &s, int G, int R, int qt) {
     return max(1, (tile_keys(s, G, R, qt) + kKeys - 1) / kKeys);
 }
 
-// pre[b] = units of the sequences before b, for all of them: every CTA forms
-// it, a thread a sequence (a warp, for a sequence of many row tiles). Returns
-// the total, below 2^31 (more is refused as a value out of range).
-template <int kThreads, int kKeys>
-__device__ int scan_units(const Attn &p, int R, int *pre, long long *warp_sums) {
-    long long base = 0;
-    for (int b0 = 0; b0 < p.b.B; b0 += kThreads) {
-        const int b = b0 + threadIdx.x;
-        long long n = 0;
-        Seq s{0, 0, 0};
-        if (b < p.b.B) s = seq_of(p.b, b, p.ctrl);
-        const int tiles = (s.nq * p.G + R - 1) / R;
-        if (tiles <= 2)
-            for (int qt = 0; qt < tiles; ++qt) n += tile_units<kKeys>(s, p.G, R, qt);
-        for (uint32_t many = __ballot_sync(0xffffffffu, tiles > 2); many; many &= many - 1) {
-            const int src = __ffs(many) - 1;
-            const Seq o{0, __shfl_sync(0xffffffffu, s.nq, src), __shfl_sync(0xffffffffu, s.len, src)};
-            const int ot = (o.nq * p.G + R - 1) / R;
-            long long m = 0;
-            for (int qt = threadIdx.x & 31; qt < ot; qt += 32) m += tile_units<kKeys>(o, p.G, R, qt);
+// The units of one head of a sequence, leading ones included. A whole warp calls
+// it, each lane with a sequence of its own (many row tiles: all lanes together).
+template <int kKeys, int kLead>
+__device__ long long head_units(const Attn &p, const Seq &s, int R) {
+    const int tiles = (s.nq * p.G + R - 1) / R, lane = threadIdx.x & 31;
+    long long n = 0;
+    if (tiles <= 2)
+        for (int qt = 0; qt < tiles; ++qt) n += tile_units<kKeys>(s, p.G, R, qt) + kLead;
+    for (uint32_t many = __ballot_sync(0xffffffffu, tiles > 2); many; many &= many - 1) {
+        const int src = __ffs(many) - 1;
+        const Seq o{0, __shfl_sync(0xffffffffu, s.nq, src), __shfl_sync(0xffffffffu, s.len, src)};
+        const int ot = (o.nq * p.G + R - 1) / R;
+        long long m = 0;
+        for (int qt = lane; qt < ot; qt += 32) m += tile_units<kKeys>(o, p.G, R, qt) + kLead;
 #pragma unroll
-            for (int x = 16; x > 0; x >>= 1) m += __shfl_xor_sync(0xffffffffu, m, x);
-            if ((threadIdx.x & 31) == src) n = m;
-        }
-        n *= p.c.Hkv;
-        long long inc = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-            if ((threadIdx.x & 31) >= o) inc += v;
-        }
-        if ((threadIdx.x & 31) == 31) warp_sums[threadIdx.x >> 5] = inc;
-        __syncthreads();
-        long long before = base;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < (int)(threadIdx.x >> 5)) before += warp_sums[w];
-            base += warp_sums[w];
-        }
-        if (b < p.b.B) pre[b] = (int)(before + inc - n);
-        if (b0 + kThreads < p.b.B) __syncthreads();
+        for (int x = 16; x > 0; x >>= 1) m += __shfl_xor_sync(0xffffffffu, m, x);
+        if (lane == src) n = m;
     }
-    if (threadIdx.x == 0) pre[p.b.B] = (int)base;
-    __syncthreads();
-    if (base >= (1ll << 31)) {
-        set_error(p.ctrl, MOE_ERR_DEVICE);
-        return 0;
-    }
-    return (int)base;
+    return n;
 }
 
 // The shares of C CTAs in U units: CTA c begins at floor(U c / C).
@@ -188,17 +161,17 @@ struct Shares {
 
 struct Item {
     int b, h, qt;
-    int units, first;     // of the item; its first unit
+    int units, first, span;   // units of keys; the first of its units and their number, leading ones included
     Seq s;
 };
 
 // The row tile of a sequence and head (whose units begin at `at`) that holds unit u; a
 // whole warp calls it.
-template <int kKeys>
+template <int kKeys, int kLead>
 __device__ void find_tile(const Attn &p, int R, int u, int at, Item &it) {
     const int tiles = (it.s.nq * p.G + R - 1) / R, lane = threadIdx.x & 31;
     for (int q0 = 0;; q0 += 32) {   // 32 at a time
-        const int n = q0 + lane < tiles ? tile_units<kKeys>(it.s, p.G, R, q0 + lane) : 0;
+        const int n = q0 + lane < tiles ? tile_units<kKeys>(it.s, p.G, R, q0 + lane) + kLead : 0;
         int inc = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -209,7 +182,8 @@ __device__ void find_tile(const Attn &p, int R, int u, int at, Item &it) {
         if (here || q0 + 32 >= tiles) {
             const int src = here ? __ffs(here) - 1 : 0;
             it.qt = q0 + src;
-            it.units = __shfl_sync(0xffffffffu, n, src);
+            it.span = __shfl_sync(0xffffffffu, n, src);
+            it.units = it.span - kLead;
             it.first = at + __shfl_sync(0xffffffffu, inc - n, src);
             return;
         }
@@ -217,69 +191,36 @@ __device__ void find_tile(const Attn &p, int R, int u, int at, Item &it) {
     }
 }
 
-// The item that holds unit u (u below the total); a whole warp calls it.
-template <int kKeys>
-__device__ Item find_item(const Attn &p, int R, const int *pre, int u) {
-    Item it;
-    int lo = 0;
-    for (int hi = p.b.B; hi - lo > 1;) {
-        const int mid = (lo + hi) >> 1;
-        if (pre[mid] <= u) lo = mid;
-        else hi = mid;
-    }
-    it.b = lo;   // (sequences without units share their successor's pre: the last of them is the one)
-    it.s = seq_of(p.b, lo, p.ctrl);
-    const int per_head = (pre[lo + 1] - pre[lo]) / p.c.Hkv;
-    it.h = (u - pre[lo]) / per_head;
-    const int at = pre[lo] + it.h * per_head;
-    find_tile<kKeys>(p, R, u, at, it);
-    return it;
-}
-
-// The shares, and the first item of CTA c's (where it has one: c < C). Up to
-// kThreads sequences, the thread that has the item's sequence in its registers
-// passes it on; beyond that it is searched for. Ends with the item in every
-// thread, but not with a barrier.
-template <int kThreads, int kKeys>
+// The shares, and the item that CTA c's begins in (where it has a share: c < C).
+// All threads call it; it begins and ends with a barrier or more, between which
+// `pre` is used where there are more than kThreads sequences. A total of 2^31
+// units is refused as a value out of range.
+template <int kThreads, int kKeys, int kLead>
 __device__ Shares first_item(const Attn &p, int R, int c, int *pre, long long *warp_sums, Item &shared, Item &it) {
-    if (p.b.B > kThreads) {
-        const int U = scan_units<kThreads, kKeys>(p, R, pre, warp_sums);
-        Shares shares(U, U == 0 ? 1 : min((int)gridDim.x, U));
-        if (U == 0) shares.C = 0;
-        if (c < shares.C) it = find_item<kKeys>(p, R, pre, shares.begin(c));
-        return shares;
-    }
-    const int b = threadIdx.x, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long total = 0, before = 0, per_head = 0, n = 0;
     Seq s{0, 0, 0};
-    if (b < p.b.B) s = seq_of(p.b, b, p.ctrl);
-    const int tiles = (s.nq * p.G + R - 1) / R;
-    long long per_head = 0;
-    if (tiles <= 2)
-        for (int qt = 0; qt < tiles; ++qt) per_head += tile_units<kKeys>(s, p.G, R, qt);
-    for (uint32_t many = __ballot_sync(0xffffffffu, tiles > 2); many; many &= many - 1) {
-        const int src = __ffs(many) - 1;
-        const Seq o{0, __shfl_sync(0xffffffffu, s.nq, src), __shfl_sync(0xffffffffu, s.len, src)};
-        const int ot = (o.nq * p.G + R - 1) / R;
-        long long m = 0;
-        for (int qt = lane; qt < ot; qt += 32) m += tile_units<kKeys>(o, p.G, R, qt);
+    for (int b0 = 0; b0 < p.b.B; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        s = b < p.b.B ? seq_of(p.b, b, p.ctrl) : Seq{0, 0, 0};
+        per_head = head_units<kKeys, kLead>(p, s, R);
+        n = per_head * p.c.Hkv;
+        long long inc = n;
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) m += __shfl_xor_sync(0xffffffffu, m, x);
-        if (lane == src) per_head = m;
-    }
-    const long long n = per_head * p.c.Hkv;
-    long long inc = n;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        if (b0 > 0) __syncthreads();   // (the last round's sums have been read)
+        if (lane == 31) warp_sums[warp] = inc;
+        __syncthreads();
+        before = total + inc - n;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-    }
-    if (lane == 31) warp_sums[threadIdx.x >> 5] = inc;
-    __syncthreads();
-    long long total = 0, before = inc - n;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < (int)(threadIdx.x >> 5)) before += warp_sums[w];
-        total += warp_sums[w];
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += warp_sums[w];
+            total += warp_sums[w];
+        }
+        if (p.b.B > kThreads && b < p.b.B) pre[b] = (int)before;
     }
     if (total >= (1ll << 31)) {
         set_error(p.ctrl, MOE_ERR_DEVICE);
@@ -287,30 +228,48 @@ __device__ Shares first_item(const Attn &p, int R, int c, int *pre, long long *w
     }
     Shares shares((int)total, total == 0 ? 1 : (int)min((long long)gridDim.x, total));
     if (total == 0) shares.C = 0;
+    if (p.b.B > kThreads) __syncthreads();
     if (c < shares.C) {
         const int u = shares.begin(c);
-        const bool mine = before <= u && u < before + n;
-        const uint32_t who = __ballot_sync(0xffffffffu, mine);
-        if (who) {   // (one warp) its lanes look through the sequence's row tiles
-            const int src = __ffs(who) - 1;
-            const int ph = (int)__shfl_sync(0xffffffffu, per_head, src), at0 = (int)__shfl_sync(0xffffffffu, before, src);
-            Item x;
+        Item x;
+        bool look = false;   // this warp looks for the row tile
+        int at = 0;
+        if (p.b.B <= kThreads) {   // the warp that has the sequence in its registers
+            const uint32_t who = __ballot_sync(0xffffffffu, before <= u && u < before + n);
+            const int src = who ? __ffs(who) - 1 : 0;
+            look = who != 0;
             x.b = (threadIdx.x & ~31) + src;
             x.s = Seq{__shfl_sync(0xffffffffu, s.q0, src), __shfl_sync(0xffffffffu, s.nq, src), __shfl_sync(0xffffffffu, s.len, src)};
-            x.h = (u - at0) / ph;
-            find_tile<kKeys>(p, R, u, at0 + x.h * ph, x);
+            per_head = __shfl_sync(0xffffffffu, per_head, src);
+            at = (int)__shfl_sync(0xffffffffu, before, src);
+        } else if (warp == 0) {
+            int lo = 0;
+            for (int hi = p.b.B; hi - lo > 1;) {
+                const int mid = (lo + hi) >> 1;
+                if (pre[mid] <= u) lo = mid;
+                else hi = mid;
+            }
+            look = true;
+            x.b = lo;   // (sequences without units share their successor's pre: the last of them is the one)
+            x.s = seq_of(p.b, lo, p.ctrl);
+            at = pre[lo];
+            per_head = ((lo + 1 < p.b.B ? pre[lo + 1] : (int)total) - at) / p.c.Hkv;
+        }
+        if (look) {
+            x.h = (u - at) / (int)per_head;
+            find_tile<kKeys, kLead>(p, R, u, at + x.h * (int)per_head, x);
             if (lane == 0) shared = x;
         }
-        __syncthreads();
-        it = shared;
     }
+    __syncthreads();
+    if (c < shares.C) it = shared;
     return shares;
 }
 
 // The item after `it`, where there is one.
-template <int kKeys>
+template <int kKeys, int kLead>
 __device__ void next_item(const Attn &p, int R, Item &it) {
-    it.first += it.units;
+    it.first += it.span;
     if ((it.qt + 1) * R < it.s.nq * p.G) {
         ++it.qt;
     } else {
@@ -322,7 +281,17 @@ __device__ void next_item(const Attn &p, int R, Item &it) {
         }
     }
     it.units = tile_units<kKeys>(it.s, p.G, R, it.qt);
+    it.span = it.units + kLead;
 }
+
+// 16 bytes of the cache into shared memory, asynchronously; zeros where there are none.
+__device__ inline void copy16(void *dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ inline void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All of the thread's copies but those of the last N groups have arrived.
+template <int N>
+__device__ inline void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ inline uint32_t bf16x2_of(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);

@@ -42,6 +42,7 @@ namespace {
 using namespace kv4;
 
 constexpr int kKeys = 128;   // keys of a unit: a warpgroup's turn
+constexpr int kLead = 2;     // an item's start and end take about 9000 clocks, a unit 3900
 constexpr uint32_t kNibs = 0x0F0F0F0Fu;
 
 template <int D, int R>
@@ -225,15 +226,6 @@ __device__ inline void reduce_rows(const float (&v)[R], float *to) {
     if ((lane & (32 / R - 1)) == 0) to[row] = x[0];
 }
 
-// 16 bytes of the cache into shared memory, asynchronously; zeros where there are none.
-__device__ inline void copy16(void *dst, const void *src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-__device__ inline void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All of the thread's copies but those of the last N groups have arrived.
-template <int N>
-__device__ inline void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 template <int D, int R>
 __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kPerSm) kv4_decode_kernel(Attn p) {
     using Cfg = DecodeCfg<D, R>;
@@ -259,24 +251,28 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
     }
     const int c = blockIdx.x;
     Item it;
-    const Shares shares = first_item<Cfg::kThreads, kKeys>(p, R, c, s_pre, sh.sums, sh.first, it);
+    const Shares shares = first_item<Cfg::kThreads, kKeys, kLead>(p, R, c, s_pre, sh.sums, sh.first, it);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tcol = sh.tmem, tlane = tcol + ((uint32_t)(warp * 32) << 16);
-    if (c >= shares.C) {
+    // the units of keys of an item in this CTA's share
+    const int u_end = c < shares.C ? shares.begin(c + 1) : 0;
+    int st0 = 0, st1 = 0;
+    if (c < shares.C) {
+        st0 = max(shares.begin(c) - it.first - kLead, 0);
+        st1 = min(it.units, u_end - it.first - kLead);
+    }
+    if (st1 <= st0) {   // (a share that ends among leading units has nothing to do)
         if (tid == 0) p.begun[c].last = 0;
         if (warp == 0) tc::dealloc(tcol, Cfg::kCols);
         return;
     }
-    int u = shares.begin(c);
-    const int u_end = shares.begin(c + 1);
     uint32_t n_s = 0, n_o = 0;   // products of scores and of values waited for
 
     // ---- a unit's place in the cache. A warp's 32 keys are two runs of 16, each in one
     // page (page sizes are multiples of 16): lane i knows the run of keys 16 (i / 16) ...
     constexpr uint32_t kNone = 0xffffffffu;   // no such keys, or a page that does not exist: they read as zero
-    int st0 = u - it.first, st1 = min(it.units, u_end - it.first);   // the units of the item in this CTA's share
     const int run = warp * 32 + (lane & 16);
     auto page_of = [&](int st) {
         const int key = st * kKeys + run;
@@ -619,12 +615,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
         // ---- the next item's first copies, then this one's rows
         const Item done = it;
         const bool first_part = st0 == 0, whole = first_part && st1 == it.units;
-        u = it.first + st1;
-        const bool last_item = u >= u_end;
+        bool last_item = it.first + it.span >= u_end;
         if (!last_item) {
-            next_item<kKeys>(p, R, it);
+            next_item<kKeys, kLead>(p, R, it);
+            last_item = u_end - it.first <= kLead;
+        }
+        if (!last_item) {
             st0 = 0;
-            st1 = min(it.units, u_end - u);
+            st1 = min(it.units, u_end - it.first - kLead);
             page0 = page_of(0);
             page1 = page_of(1);
         }
@@ -670,7 +668,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
         if (tid == 0) {
             if (!whole) part[2 * R] = __int_as_float(F);
             if (last_item)
-                p.begun[c] = Begun{first_part && !whole ? shares.holder(done.first + done.units - 1) : 0, done.s.q0, done.h, done.qt, rows_done, {0, 0, 0}};
+                p.begun[c] = Begun{first_part && !whole ? shares.holder(done.first + done.span - 1) : 0, done.s.q0, done.h, done.qt, rows_done, {0, 0, 0}};
         }
         if (last_item) break;
     }

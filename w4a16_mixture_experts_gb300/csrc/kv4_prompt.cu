@@ -8,11 +8,14 @@
 // tiles of 128 that alternate, so that the tensor core works on one while the
 // other's softmax runs:
 //   warps 0-3, 4-7   a softmax warpgroup for each tile, a thread a row: scores
-//                    from tensor memory into registers, probabilities back as
-//                    fp16 in the same columns (the A operand of the second product)
-//   warps 8-11       a thread a key: its K and V row from the cache's pages into
-//                    shared memory as fp16, 128 keys a stage, two stages each
-//   warp 12          issues the products
+//                    from tensor memory, probabilities back as fp16 in the same
+//                    columns (the A operand of the second product)
+//   warps 8-11       a thread a key: its K row from the cache's pages into shared
+//                    memory as fp16, 128 keys a stage, two stages
+//   warps 12-15      the same for V (one warpgroup for both was what the tensor
+//                    core waited for: 4200 clocks a stage of its 2048)
+//   warp 16          issues the products
+// The codes come by cp.async, a warp its own 32 keys, a stage ahead of their use.
 // S = Q K^T has both operands K-major in the 128-byte swizzle; O += P V takes V
 // from the same row-major form as an MN-major operand, so that nothing is
 // transposed. Sums stay in tensor memory in fp32 over all keys; they are
@@ -36,17 +39,22 @@ using namespace kv4;
 constexpr int kKeys = 128;       // keys of a unit: one stage
 constexpr int kTileRows = 128, kR = kPromptRows;
 static_assert(kR == 2 * kTileRows, "two tiles");
-constexpr int kThreads = 512;    // (three warps of the last warpgroup only take part in its register split)
-constexpr int kWK = 8, kWMma = 12;
+constexpr int kThreads = 640;    // (three warps of the last warpgroup only take part in its register split)
+constexpr int kWK = 8, kWV = 12, kWMma = 16;
 constexpr int kStages = 2;
-// registers a thread after the split: 256 x 176 + 128 x 80 + 128 x 80 = 512 x 128
-constexpr int kRegsSoft = 176, kRegsDeq = 80, kRegsMma = 80, kRegsLaunch = 128;
-static_assert(256 * kRegsSoft + 128 * kRegsDeq + 128 * kRegsMma <= kThreads * kRegsLaunch, "register split");
+// registers a thread after the split: 256 x 128 + 256 x 80 + 128 x 64 = 640 x 96
+constexpr int kRegsSoft = 128, kRegsDeq = 80, kRegsMma = 64, kRegsLaunch = 96;
+static_assert(256 * kRegsSoft + 256 * kRegsDeq + 128 * kRegsMma <= kThreads * kRegsLaunch, "register split");
+// An item's start and end take about 9000 clocks, a stage 4000 (D = 128) or 2000.
+template <int D>
+constexpr int kLead = D == 128 ? 2 : 4;
 
 template <int D>
 struct PromptCfg {
     static constexpr int kTile = 128 * D * 2;      // bytes of a fp16 tile of 128 rows: blocks of 64 columns, 16 KB each
-    static constexpr int kSmem = (2 + 2 * kStages) * kTile;
+    static constexpr int kChunks = D / 32;         // 16-byte pieces of a row of codes
+    static constexpr int kRaw = 128 * D / 2;       // bytes of a stage's codes, K or V
+    static constexpr int kSmem = (2 + 2 * kStages) * kTile + 2 * kRaw;
 };
 
 struct Bars {
@@ -100,6 +108,18 @@ __device__ inline uint32_t idesc_f16(int N, bool b_mn) {
     return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
+// 32 columns of the thread's row.
+__device__ inline void ld32(uint32_t taddr, float (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+          "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
 // The loads' registers are not to be read before the wait: it passes them on.
 __device__ inline void wait_ld(float (&v)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -109,6 +129,14 @@ __device__ inline void wait_ld(float (&v)[32]) {
                    "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
                  :
                  : "memory");
+}
+
+__device__ inline void st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
 }
 
 // 16 columns of a thread's row of sums, times f.
@@ -123,11 +151,7 @@ __device__ inline void rescale16(uint32_t taddr, float f) {
         : "memory");
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
+    st16(taddr, v);
 }
 
 __device__ inline void fma2(float &a, float &b, float c, float d) {   // (a, b) = (a, b) * c + d
@@ -168,13 +192,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
     using Cfg = PromptCfg<D>;
     extern __shared__ uint8_t s_dyn[];
     uint8_t *const sQ = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(s_dyn) + 1023) & ~(uintptr_t)1023);
-    uint8_t *const sK = sQ + 2 * Cfg::kTile, *const sV = sK + kStages * Cfg::kTile;
-    int *const s_pre = reinterpret_cast<int *>(sV + kStages * Cfg::kTile);
+    uint8_t *const sK = sQ + 2 * Cfg::kTile, *const sV = sK + kStages * Cfg::kTile, *const s_raw = sV + kStages * Cfg::kTile;
+    int *const s_pre = reinterpret_cast<int *>(sK);   // (needed only before the first operand is written)
+    static_assert(sizeof(int) * 4096 <= kStages * Cfg::kTile, "prefix");
     __shared__ Bars bars;
     __shared__ long long s_sums[kThreads / 32];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
-    __shared__ int s_E[4], s_F[4], s_red[2][2][4];   // a stage's K exponent, V exponent so far (rings of 4 stages)
+    __shared__ Item s_first;
+    __shared__ int s_E[4], s_F[4], s_red[2][2][2][4];   // a stage's K exponent, V exponent so far (rings of 4 stages)
+    __shared__ alignas(16) uint16_t s_scales[8][3][2][32];   // of a warp's stages in turn: K's, V's
     volatile int *const abort_flag = &s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -196,14 +223,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
     }
     pdl_wait();
     pdl_launch_dependents();
-    const int U = scan_units<kThreads, kKeys>(p, kR, s_pre, s_sums);
-    const Shares shares(U, min((int)gridDim.x, max(1, U)));
     const int c = blockIdx.x;
-    if (c >= shares.C || U == 0) {   // (the whole CTA)
+    Item it;
+    const Shares shares = first_item<kThreads, kKeys, kLead<D>>(p, kR, c, s_pre, s_sums, s_first, it);
+    const int u_begin = c < shares.C ? shares.begin(c) : 0, u_end = c < shares.C ? shares.begin(c + 1) : 0;
+    // the stages of an item in this CTA's share: [st0, st1)
+    auto stages_of = [&](const Item &x, int &st0, int &st1) {
+        st0 = max(u_begin - x.first - kLead<D>, 0);
+        st1 = min(x.units, u_end - x.first - kLead<D>);
+        return st1 > st0;
+    };
+    int st0, st1;
+    if (c >= shares.C || !stages_of(it, st0, st1)) {   // (the whole CTA; a share that ends among leading units has nothing to do)
         if (threadIdx.x == 0) p.begun[c].last = 0;
         return;
     }
-    const int u_begin = shares.begin(c), u_end = shares.begin(c + 1);
+    // the next item with stages in the share; false: there is none
+    auto go_on = [&]() {
+        if (it.first + it.span >= u_end) return false;
+        next_item<kKeys, kLead<D>>(p, kR, it);
+        return stages_of(it, st0, st1);
+    };
     if (warp == kWMma) {
         tc::alloc(&s_tmem, 512);
         tc::relinquish();
@@ -221,14 +261,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
         const uint32_t tS = tmem + lanes + wg * 128, tO = tmem + lanes + 256 + wg * D;
         uint32_t g = 0, gs = 0, n_item = 0;   // stages so far (all items; of this tile's), items
         bool ok = true;
-        Item it = find_item<kKeys>(p, kR, s_pre, u_begin);
-        for (int u = u_begin;; next_item<kKeys>(p, kR, it), ++n_item) {
-            const int st0 = u - it.first, st1 = min(it.units, u_end - it.first);
+        for (;; ++n_item) {
             const int rows = min(kR, it.s.nq * p.G - it.qt * kR);
             const int rr = it.qt * kR + r, qi = rr / p.G, head = it.h * p.G + rr - qi * p.G;
             const bool mine = wg * kTileRows < rows;   // (the whole warpgroup) this tile has rows
             // ---- the row's query
-            float c_row = 0.f;
+            float c_row = 0.f, l0 = 0.f, l1 = 0.f;
             int lim = 0;
             {
                 uint4 x[D / 8];
@@ -247,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                 if (p.scale < 0.f) f = -f;   // so that the largest product is the largest score
                 if (there) lim = it.s.len - it.s.nq + qi + 1;
                 c_row = fabsf(p.scale) * kLog2e * pow2_biased(e);
+                if (big >= 0x7F80u) l0 = __uint_as_float(0x7fc00000u);   // a query that is not finite: NaN
                 uint8_t *const tile = sQ + wg * Cfg::kTile;
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) {
@@ -266,34 +305,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                 if (lane == 0) mbar_arrive(&bars.q_full);
             }
             const int least = __reduce_min_sync(0xffffffffu, lim);
-            float m = kNoMax, l0 = 0.f, l1 = 0.f;
+            float m = kNoMax;
             int F = 1;
             for (int st = st0; st < st1 && ok; ++st, ++g) {
                 if (!mine) continue;
                 if (!(ok = wait(&bars.s_full[wg], gs & 1, abort_flag))) break;
                 ++gs;
                 tc::fence_after();
-                float s[4][32];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) tc::ld_32x32b_x32(tS + i * 32, s[i]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) wait_ld(s[i]);
                 const int E = s_E[g & 3], Fn = s_F[g & 3];
                 const float ct = fmaxf(c_row * pow2_biased(E), 1e-37f);
-                if (st * kKeys + kKeys > least) {
-                    const int left = lim - st * kKeys;   // keys of the stage that the row sees
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                const bool edge = st * kKeys + kKeys > least;
+                const int left = lim - st * kKeys;   // keys of the stage that the row sees
+                // 32 scores at a time, the next 32 under way: once for the maximum, once for the
+                // probabilities (128 of them in registers left too few for the other warps)
+                float s[2][32], mx[4];
+                auto hide = [&](float (&x)[32], int i) {
+                    if (edge) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (i * 32 + j >= left) s[i][j] = -INFINITY;
-                }
-                float mx[4];
+                            if (i * 32 + j >= left) x[j] = -INFINITY;
+                    }
+                };
+                ld32(tS, s[0]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    mx[i] = s[i][0];
+                    float(&x)[32] = s[i & 1];
+                    wait_ld(x);
+                    ld32(tS + (i + 1) % 4 * 32, s[(i + 1) & 1]);   // (after the last: the first again)
+                    hide(x, i);
+                    mx[i] = x[0];
 #pragma unroll
-                    for (int j = 1; j < 32; ++j) mx[i] = fmaxf(mx[i], s[i][j]);
+                    for (int j = 1; j < 32; ++j) mx[i] = fmaxf(mx[i], x[j]);
                 }
                 const float big = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * ct;
                 if (__any_sync(0xffffffffu, big > m + 8.f || Fn != F)) {
@@ -311,19 +353,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                     }
                 }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {   // 64 keys at a time
-                    uint32_t pr[32];
+                for (int i = 0; i < 4; ++i) {
+                    float(&x)[32] = s[i & 1];
+                    wait_ld(x);
+                    if (i < 3) ld32(tS + (i + 1) * 32, s[(i + 1) & 1]);
+                    hide(x, i);
+                    uint32_t pr[16];
 #pragma unroll
-                    for (int j = 0; j < 64; j += 2) {
-                        float &x = s[h * 2 + (j >> 5)][j & 31], &y = s[h * 2 + (j >> 5)][(j & 31) + 1];
-                        fma2(x, y, ct, -m);
-                        x = exp2_approx(x);
-                        y = exp2_approx(y);
-                        add2(l0, l1, x, y);
-                        const __half2 v = __floats2half2_rn(x, y);
+                    for (int j = 0; j < 32; j += 2) {
+                        fma2(x[j], x[j + 1], ct, -m);
+                        x[j] = exp2_approx(x[j]);
+                        x[j + 1] = exp2_approx(x[j + 1]);
+                        add2(l0, l1, x[j], x[j + 1]);
+                        const __half2 v = __floats2half2_rn(x[j], x[j + 1]);
                         pr[j >> 1] = *reinterpret_cast<const uint32_t *>(&v);
                     }
-                    tc::st_32x32b_x32(tS + h * 32, pr);
+                    st16(tS + i * 16, pr);   // (in columns whose scores have been read)
                 }
                 tc::wait_st();
                 tc::fence_before();
@@ -342,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
                     float o[32];
-                    tc::ld_32x32b_x32(tO + i * 32, o);
+                    ld32(tO + i * 32, o);
                     wait_ld(o);
                     if (r < rows) {
 #pragma unroll
@@ -371,115 +416,128 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                 }
             }
             tc::fence_before();
-            u = it.first + st1;
-            if (threadIdx.x == 0 && (!ok || u >= u_end)) {
-                const bool goes_on = ok && st0 == 0 && !whole;
-                p.begun[c] = Begun{goes_on ? shares.holder(it.first + it.units - 1) : 0, it.s.q0, it.h, it.qt, rows, {0, 0, 0}};
-            }
             if (!ok) {
                 *abort_flag = 1;
                 if (lane == 0) set_error(p.ctrl, MOE_ERR_TIMEOUT);
+            }
+            const Begun begun{ok && st0 == 0 && !whole ? shares.holder(it.first + it.span - 1) : 0, it.s.q0, it.h, it.qt, rows, {0, 0, 0}};
+            if (!ok || !go_on()) {
+                if (threadIdx.x == 0) p.begun[c] = begun;
                 break;
             }
-            if (u >= u_end) break;
         }
     } else if (warp < kWMma) {
-        // ------------------------------------------------------------ keys and values, a thread a key
+        // ------------------------------------------------------------ keys (warps 8-11) or values, a thread a key
         regs_dec<kRegsDeq>();
-        const int r = threadIdx.x & 127, w4 = warp & 3;
+        const bool keys = warp < kWV;
+        const int r = threadIdx.x & 127, w4 = warp & 3, run = w4 * 32 + (lane & 16);
+        uint8_t *const raw = s_raw + (keys ? 0 : Cfg::kRaw) + w4 * (32 * D / 2), *const tiles = keys ? sK : sV;
+        uint64_t *const full = keys ? bars.k_full : bars.v_full, *const empty = keys ? bars.k_empty : bars.v_empty;
+        uint16_t(*const scales)[2][32] = s_scales[warp - kWK];
+        // A warp's 32 keys are two runs of 16, each in one page: lane i knows the run of keys
+        // 16 (i / 16) ... and the warp copies 512 bytes at a time, the 16-byte pieces of a row
+        // turned by the row, so that lanes that read a row each meet no bank twice.
+        constexpr uint32_t kNone = 0xffffffffu;   // no such keys, or a page that does not exist: they read as zero
+        auto turned = [](int x) { return D == 128 ? x >> 1 & 3 : x >> 2 & 1; };
+        const int copy_to = (lane / Cfg::kChunks * Cfg::kChunks + (lane % Cfg::kChunks ^ turned(lane / Cfg::kChunks))) * 16;
+        const char *const from = reinterpret_cast<const char *>(keys ? p.c.k_codes : p.c.v_codes) + lane * 16;
+        const uint16_t *const scales_from = ((lane & 2) ? p.c.v_scales : p.c.k_scales) + (lane & 1) * 8;
         uint32_t g = 0;
         bool ok = true;
-        Item it = find_item<kKeys>(p, kR, s_pre, u_begin);
-        for (int u = u_begin; ok; next_item<kKeys>(p, kR, it)) {
-            const int st0 = u - it.first, st1 = min(it.units, u_end - it.first);
+        for (;;) {
+            const int len = it.s.len;
             const int32_t *table = p.b.table + (size_t)it.b * p.b.max_pages;
-            const int len = it.s.len, pmask = (1 << p.b.shift) - 1;
             auto page_of = [&](int st) {
-                const int key = st * kKeys + r;
-                return st < st1 && key < len ? __ldg(table + (key >> p.b.shift)) : -1;
+                const int key = st * kKeys + run;
+                return st < st1 && key < len ? ld_here(table + (key >> p.b.shift)) : -1;
             };
-            uint4 kw[D / 32], vw[D / 32];
-            uint16_t ks = 0, vs = 0;
-            size_t row = 0;
-            auto place = [&](int st, int page) {   // the thread's row of stage st; its scales
-                const int key = st * kKeys + r;
-                const bool in = st < st1 && key < len, fine = in && (unsigned)page < (unsigned)p.c.n_pages;
-                if (in && !fine) set_error(p.ctrl, MOE_ERR_DEVICE);
-                row = fine ? (((size_t)page * p.c.Hkv + it.h) << p.b.shift) + (key & pmask) : 0;
-                ks = fine ? __ldg(p.c.k_scales + row) : 0;
-                vs = fine ? __ldg(p.c.v_scales + row) : 0;
-            };
-            auto load = [&](uint4 (&w)[D / 32], const int32_t *codes) {
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) w[i] = ld_nc_v4(codes + row * (D / 8) + i * 4);
-            };
-            auto store = [&](uint8_t *tile, const uint4 (&w)[D / 32], __half2 s) {
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<uint4 *>(chunk_at<D>(tile, r, i * 4 + j)) = dequant_chunk(x[j], s);
+            auto place = [&](int st, int page) {   // the run's first row (row indexes are below 2^32 - 1)
+                const int key = st * kKeys + run;
+                if (st >= st1 || key >= len) return kNone;
+                if ((unsigned)page >= (unsigned)p.c.n_pages) {
+                    set_error(p.ctrl, MOE_ERR_DEVICE);
+                    return kNone;
                 }
+                return (((uint32_t)page * (uint32_t)p.c.Hkv + (uint32_t)it.h) << p.b.shift) + (uint32_t)(key & ((1 << p.b.shift) - 1));
             };
-            place(st0, page_of(st0));
-            load(kw, p.c.k_codes);
-            load(vw, p.c.v_codes);
-            int page = page_of(st0 + 1);
-            int F = 1;
+            auto copy = [&](uint32_t at, int slot) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t src = __shfl_sync(0xffffffffu, at, 16 * i);
+                    const bool there = src != kNone;
+                    const char *x = from + (size_t)(there ? src : 0) * (D / 2);
+#pragma unroll
+                    for (int k = 0; k < D / 64; ++k) copy16(raw + copy_to + i * (8 * D) + k * 512, x + k * 512, there);
+                }
+                // a run's scales are 32 bytes: lanes 0-1 and 16-17 copy K's, 2-3 and 18-19 V's
+                if ((lane & 15) < 4)
+                    copy16(&scales[slot][lane >> 1 & 1][(lane & 16) + (lane & 1) * 8], scales_from + (at != kNone ? at : 0), at != kNone);
+                copies_commit();
+            };
+            uint32_t at0 = place(st0, page_of(st0)), at1 = kNone;
+            int page = page_of(st0 + 1), slot = 0, F = 1;
+            copy(at0, 0);
             for (int st = st0; st < st1; ++st, ++g) {
                 const int b = g % kStages;
-                const uint32_t ph = (g / kStages) & 1;
-                ok = ok && wait(&bars.k_empty[b], ph ^ 1, abort_flag);
+                copies_wait<0>();
+                __syncwarp();
+                uint4 w[Cfg::kChunks];
+#pragma unroll
+                for (int i = 0; i < Cfg::kChunks; ++i) w[i] = lds_v4(raw + (lane * Cfg::kChunks + (i ^ turned(lane))) * 16);
+                const bool there = at0 != kNone && st * kKeys + r < len;
+                const uint16_t ks = there ? scales[slot][0][lane] : (uint16_t)0, vs = there ? scales[slot][1][lane] : (uint16_t)0;
+                __syncwarp();
+                slot = slot == 2 ? 0 : slot + 1;
+                if (st + 1 < st1) {
+                    at1 = place(st + 1, page);
+                    page = page_of(st + 2);
+                    copy(at1, slot);
+                }
+                at0 = at1;
+                ok = wait(&empty[b], ((g / kStages) & 1) ^ 1, abort_flag);
                 // ---- the stage's exponents; a row that was not finite: K becomes NaN, V zero
                 const bool bad = !finite_bits(ks) || !finite_bits(vs);
                 const float kf = bad ? 0.f : bf16_bits_to_f32(ks), vf = bad ? 0.f : bf16_bits_to_f32(vs);
                 const uint32_t ek = __reduce_max_sync(0xffffffffu, __float_as_uint(kf) >> 23 & 0xFFu);
                 const uint32_t ev = __reduce_max_sync(0xffffffffu, __float_as_uint(vf) >> 23 & 0xFFu);
+                int(&red)[2][4] = s_red[!keys][g & 1];
                 if (lane == 0) {
-                    s_red[g & 1][0][w4] = (int)ek;
-                    s_red[g & 1][1][w4] = (int)ev;
+                    red[0][w4] = (int)ek;
+                    red[1][w4] = (int)ev;
                 }
-                if (!(ok = bar_and(2, 128, ok))) break;
+                if (!(ok = bar_and(keys ? 2 : 3, 128, ok))) break;   // (for all warps of the role at once)
                 int E = 1;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    E = max(E, s_red[g & 1][0][i]);
-                    F = max(F, s_red[g & 1][1][i]);
+                    E = max(E, red[0][i]);
+                    F = max(F, red[1][i]);
                 }
                 E = min(E, 253);
                 F = min(F, 253);
-                if (r == 0) {
+                if (keys && r == 0) {
                     s_E[g & 3] = E;
                     s_F[g & 3] = F;
                 }
-                const __half2 k2 = bad ? __float2half2_rn(NAN) : __float2half2_rn(kf * pow2_biased(254 - E));
-                const __half2 v2 = __float2half2_rn(vf * pow2_biased(254 - F));
-                store(sK + b * Cfg::kTile, kw, k2);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.k_full[b]);
-                const bool more = st + 1 < st1;
-                if (more) {
-                    place(st + 1, page);
-                    load(kw, p.c.k_codes);
-                    page = page_of(st + 2);
+                const __half2 s2 = !keys ? __float2half2_rn(vf * pow2_biased(254 - F)) : bad ? __float2half2_rn(NAN) : __float2half2_rn(kf * pow2_biased(254 - E));
+#pragma unroll
+                for (int i = 0; i < Cfg::kChunks; ++i) {
+                    const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<uint4 *>(chunk_at<D>(tiles + b * Cfg::kTile, r, i * 4 + j)) = dequant_chunk(x[j], s2);
                 }
-                ok = wait(&bars.v_empty[b], ph ^ 1, abort_flag);
-                if (ok) store(sV + b * Cfg::kTile, vw, v2);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.v_full[b]);
-                if (more) load(vw, p.c.v_codes);
+                if (lane == 0) mbar_arrive(&full[b]);
             }
-            u = it.first + st1;
             if (!ok) {
                 *abort_flag = 1;
                 if (lane == 0) set_error(p.ctrl, MOE_ERR_TIMEOUT);
                 break;
             }
-            if (u >= u_end) break;
+            if (!go_on()) break;
         }
+        copies_wait<0>();
     } else {
         regs_dec<kRegsMma>();
         if (warp == kWMma) {
@@ -512,9 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                 if (elect()) tc::commit(bar);
                 __syncwarp();
             };
-            Item it = find_item<kKeys>(p, kR, s_pre, u_begin);
-            for (int u = u_begin;; next_item<kKeys>(p, kR, it), ++n_item) {
-                const int st0 = u - it.first, st1 = min(it.units, u_end - it.first);
+            for (;; ++n_item) {
                 const bool two = it.s.nq * p.G - it.qt * kR > kTileRows;
                 ok = wait(&bars.q_full, n_item & 1, abort_flag) && wait(&bars.k_full[g % kStages], (g / kStages) & 1, abort_flag);
                 if (ok) {
@@ -556,8 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                     if (lane == 0) set_error(p.ctrl, MOE_ERR_TIMEOUT);
                     break;
                 }
-                u = it.first + st1;
-                if (u >= u_end) break;
+                if (!go_on()) break;
             }
         }
     }
@@ -578,12 +633,12 @@ cudaError_t launch_one(const Attn &p, int *grid_out, cudaStream_t s) {
     }();
     if (!split_ok) return cudaErrorInvalidConfiguration;
     constexpr size_t kBase = PromptCfg<D>::kSmem + 1024;
-    const cudaError_t err = set_smem_once(fn, (int)(kBase + sizeof(int) * 4097));
+    const cudaError_t err = set_smem_once(fn, (int)kBase);
     if (err != cudaSuccess) return err;
     int grid = sm_count();
     if (grid > kMaxPromptCtas) grid = kMaxPromptCtas;
     *grid_out = grid;
-    return launch_pdl(kv4_prompt_kernel<D>, dim3((unsigned)grid), kThreads, kBase + sizeof(int) * ((size_t)p.b.B + 1), s, p);
+    return launch_pdl(kv4_prompt_kernel<D>, dim3((unsigned)grid), kThreads, kBase, s, p);
 }
 
 }  // namespace
