@@ -2,20 +2,27 @@
 // and prompt chunks), on the tensor core.
 //
 // What bounds it: 4 D flops per (query row, key), two products of which the
-// tensor core does 128 x 128 x D in 64 D clocks (D = 128: 512), against an
+// tensor core does 128 x 128 x D in 4 D clocks (D = 128: 512), against an
 // exponential for each score and the dequantisation of each key and value once
 // for every 256 rows. A CTA takes 256 rows (query, head of the group) in two
 // tiles of 128 that alternate, so that the tensor core works on one while the
 // other's softmax runs:
-//   warps 0-3, 4-7   a softmax warpgroup for each tile, a thread a row: scores
-//                    from tensor memory, probabilities back as fp16 in the same
-//                    columns (the A operand of the second product)
+//   warps 0-3, 4-7   a softmax warpgroup for each tile, a thread a row: its 128
+//                    scores from tensor memory into registers, probabilities
+//                    back as fp16 in the same columns (the A operand of the
+//                    second product)
 //   warps 8-11       a thread a key: its K row from the cache's pages into shared
 //                    memory as fp16, 128 keys a stage, two stages
 //   warps 12-15      the same for V (one warpgroup for both was what the tensor
 //                    core waited for: 4200 clocks a stage of its 2048)
 //   warp 16          issues the products
 // The codes come by cp.async, a warp its own 32 keys, a stage ahead of their use.
+// The softmax is on a tile's path between its two products, so it is what must be
+// short: the scores stay in registers (read twice from tensor memory, with 128
+// registers a thread, 4096 queries x 4096 keys x 32 heads take 875 us; as here,
+// 766), and a stage is 128 keys wide, because the scores' product reads the
+// queries again for each of its parts (64 keys wide, with the other 64 keys'
+// softmax meanwhile: 924 us).
 // S = Q K^T has both operands K-major in the 128-byte swizzle; O += P V takes V
 // from the same row-major form as an MN-major operand, so that nothing is
 // transposed. Sums stay in tensor memory in fp32 over all keys; they are
@@ -42,8 +49,8 @@ static_assert(kR == 2 * kTileRows, "two tiles");
 constexpr int kThreads = 640;    // (three warps of the last warpgroup only take part in its register split)
 constexpr int kWK = 8, kWV = 12, kWMma = 16;
 constexpr int kStages = 2;
-// registers a thread after the split: 256 x 128 + 256 x 80 + 128 x 64 = 640 x 96
-constexpr int kRegsSoft = 128, kRegsDeq = 80, kRegsMma = 64, kRegsLaunch = 96;
+// registers a thread after the split: 256 x 160 + 256 x 56 + 128 x 48 = 640 x 96
+constexpr int kRegsSoft = 160, kRegsDeq = 56, kRegsMma = 48, kRegsLaunch = 96;
 static_assert(256 * kRegsSoft + 256 * kRegsDeq + 128 * kRegsMma <= kThreads * kRegsLaunch, "register split");
 // An item's start and end take about 9000 clocks, a stage 4000 (D = 128) or 2000.
 template <int D>
@@ -314,29 +321,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                 tc::fence_after();
                 const int E = s_E[g & 3], Fn = s_F[g & 3];
                 const float ct = fmaxf(c_row * pow2_biased(E), 1e-37f);
-                const bool edge = st * kKeys + kKeys > least;
-                const int left = lim - st * kKeys;   // keys of the stage that the row sees
-                // 32 scores at a time, the next 32 under way: once for the maximum, once for the
-                // probabilities (128 of them in registers left too few for the other warps)
-                float s[2][32], mx[4];
-                auto hide = [&](float (&x)[32], int i) {
-                    if (edge) {
+                float x[128], mx[4];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (i * 32 + j >= left) x[j] = -INFINITY;
-                    }
-                };
-                ld32(tS, s[0]);
+                for (int i = 0; i < 4; ++i) ld32(tS + i * 32, *reinterpret_cast<float(*)[32]>(x + i * 32));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float(&x)[32] = s[i & 1];
-                    wait_ld(x);
-                    ld32(tS + (i + 1) % 4 * 32, s[(i + 1) & 1]);   // (after the last: the first again)
-                    hide(x, i);
-                    mx[i] = x[0];
+                for (int i = 0; i < 4; ++i) wait_ld(*reinterpret_cast<float(*)[32]>(x + i * 32));
+                if (st * kKeys + kKeys > least) {
+                    const int left = lim - st * kKeys;   // keys of the stage that the row sees
 #pragma unroll
-                    for (int j = 1; j < 32; ++j) mx[i] = fmaxf(mx[i], x[j]);
+                    for (int j = 0; j < 128; ++j)
+                        if (j >= left) x[j] = -INFINITY;
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mx[i] = x[i];
+#pragma unroll
+                for (int j = 4; j < 128; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
                 const float big = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * ct;
                 if (__any_sync(0xffffffffu, big > m + 8.f || Fn != F)) {
                     // a new maximum (or exponent of V): the row's sums so far follow it
@@ -353,22 +352,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float(&x)[32] = s[i & 1];
-                    wait_ld(x);
-                    if (i < 3) ld32(tS + (i + 1) * 32, s[(i + 1) & 1]);
-                    hide(x, i);
+                for (int i = 0; i < 128; i += 32) {
                     uint32_t pr[16];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
-                        fma2(x[j], x[j + 1], ct, -m);
-                        x[j] = exp2_approx(x[j]);
-                        x[j + 1] = exp2_approx(x[j + 1]);
-                        add2(l0, l1, x[j], x[j + 1]);
-                        const __half2 v = __floats2half2_rn(x[j], x[j + 1]);
+                        float &y = x[i + j], &z = x[i + j + 1];
+                        fma2(y, z, ct, -m);
+                        y = exp2_approx(y);
+                        z = exp2_approx(z);
+                        add2(l0, l1, y, z);
+                        const __half2 v = __floats2half2_rn(y, z);
                         pr[j >> 1] = *reinterpret_cast<const uint32_t *>(&v);
                     }
-                    st16(tS + i * 16, pr);   // (in columns whose scores have been read)
+                    st16(tS + (i >> 1), pr);
                 }
                 tc::wait_st();
                 tc::fence_before();
