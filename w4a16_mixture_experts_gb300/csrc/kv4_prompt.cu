@@ -19,7 +19,7 @@
 // The codes come by cp.async, a warp its own 32 keys, a stage ahead of their use.
 // The softmax is on a tile's path between its two products, so it is what must be
 // short: the scores stay in registers (read twice from tensor memory, with 128
-// registers a thread, 4096 queries x 4096 keys x 32 heads take 875 us; as here,
+// registers a thread, 4096 queries of 32 heads behind 12288 keys take 875 us; as here,
 // 766), and a stage is 128 keys wide, because the scores' product reads the
 // queries again for each of its parts (64 keys wide, with the other 64 keys'
 // softmax meanwhile: 924 us).
@@ -37,6 +37,8 @@
 #include "kv4_attention.cuh"
 #include "tcgen05.cuh"
 
+#include <type_traits>
+
 namespace moe {
 
 namespace {
@@ -49,8 +51,8 @@ static_assert(kR == 2 * kTileRows, "two tiles");
 constexpr int kThreads = 640;    // (three warps of the last warpgroup only take part in its register split)
 constexpr int kWK = 8, kWV = 12, kWMma = 16;
 constexpr int kStages = 2;
-// registers a thread after the split: 256 x 160 + 256 x 56 + 128 x 48 = 640 x 96
-constexpr int kRegsSoft = 160, kRegsDeq = 56, kRegsMma = 48, kRegsLaunch = 96;
+// registers a thread after the split: 256 x 160 + 256 x 64 + 128 x 32 = 640 x 96
+constexpr int kRegsSoft = 160, kRegsDeq = 64, kRegsMma = 32, kRegsLaunch = 96;
 static_assert(256 * kRegsSoft + 256 * kRegsDeq + 128 * kRegsMma <= kThreads * kRegsLaunch, "register split");
 // An item's start and end take about 9000 clocks, a stage 4000 (D = 128) or 2000.
 template <int D>
@@ -62,6 +64,9 @@ struct PromptCfg {
     static constexpr int kChunks = D / 32;         // 16-byte pieces of a row of codes
     static constexpr int kRaw = 128 * D / 2;       // bytes of a stage's codes, K or V
     static constexpr int kSmem = (2 + 2 * kStages) * kTile + 2 * kRaw;
+    // Shared addresses of the operands, known here so that their descriptors are constants: the
+    // kernel's other shared memory lies below (the kernel checks it).
+    static constexpr int kAtQ = 8192, kAtK = kAtQ + 2 * kTile, kAtV = kAtK + kStages * kTile;
 };
 
 struct Bars {
@@ -101,13 +106,13 @@ __device__ inline void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u3
 template <int N>
 __device__ inline void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// A row-major [keys][64-column blocks] tile as an MN-major operand: 64 columns
-// of a row are 128 swizzled bytes, 8 rows an atom of 1024 (the stride along K),
-// 64-column blocks 16 KB apart (the leading stride).
-__device__ inline uint64_t sdesc_mn_sw128(const void *smem_ptr) {
-    const uint32_t addr = smem_u32(smem_ptr);
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)(16384u >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
-           (uint64_t)1u << 46 | (uint64_t)2u << 61;
+// Descriptor of an operand at a shared address, 128-byte swizzle, 8 rows an atom
+// of 1024 bytes. K-major: the leading stride is not used (1). A row-major
+// [keys][64-column blocks] tile as an MN-major operand: 64 columns of a row are
+// 128 swizzled bytes, atoms follow along K, 64-column blocks lie 16 KB apart (the
+// leading stride, 1024 units of 16 bytes).
+__host__ __device__ constexpr uint64_t sdesc(uint32_t addr, uint32_t lead) {
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)lead << 16 | (uint64_t)(1024u >> 4) << 32 | (uint64_t)1u << 46 | (uint64_t)2u << 61;
 }
 
 // kind::f16, f16 operands, f32 sums; B K-major or MN-major.
@@ -198,7 +203,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
     using Cfg = PromptCfg<D>;
     extern __shared__ uint8_t s_dyn[];
-    uint8_t *const sQ = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(s_dyn) + 1023) & ~(uintptr_t)1023);
+    uint8_t *const sQ = s_dyn + (Cfg::kAtQ - smem_u32(s_dyn));
     uint8_t *const sK = sQ + 2 * Cfg::kTile, *const sV = sK + kStages * Cfg::kTile, *const s_raw = sV + kStages * Cfg::kTile;
     int *const s_pre = reinterpret_cast<int *>(sK);   // (needed only before the first operand is written)
     static_assert(sizeof(int) * 4096 <= kStages * Cfg::kTile, "prefix");
@@ -212,6 +217,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
     volatile int *const abort_flag = &s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    {
+        uint32_t size;
+        asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(size));
+        if (smem_u32(s_dyn) > Cfg::kAtQ || smem_u32(s_dyn) + size < Cfg::kAtQ + Cfg::kSmem) {   // (the whole card: the same for every CTA)
+            if (threadIdx.x == 0) {
+                set_error(p.ctrl, MOE_ERR_DEVICE);
+                p.begun[blockIdx.x].last = 0;
+            }
+            return;
+        }
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&bars.k_full[i], 4);
@@ -258,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    const uint32_t tmem = s_tmem;   // columns: S0/P0 0-127, S1/P1 128-255, O0 from 256, O1 from 256 + D
+    constexpr uint32_t tmem = 0;   // (all 512 columns: they begin at 0) columns: S0/P0 0-127, S1/P1 128-255, O0 from 256, O1 from 256 + D
 
     if (warp < kWK) {
         // ------------------------------------------------------------ softmax, a thread a row
@@ -541,24 +557,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
             const uint32_t id_s = idesc_f16(128, false), id_o = idesc_f16(D, true);
             uint32_t g = 0, gp[2] = {0, 0}, n_item = 0;
             bool ok = true;
-            auto scores = [&](int wg, int b) {
+            const std::integral_constant<int, 0> c0;
+            const std::integral_constant<int, 1> c1;
+            static_assert(kStages == 2, "buffers");
+            // Tile, stage and addresses are constants here: descriptors made from registers were kept
+            // in too many of them, and moved to where the instructions take them from each time
+            // (the figure above: 766 -> 733 us).
+            auto scores = [&](auto wg_c, auto b_c) {
+                constexpr int wg = decltype(wg_c)::value, b = decltype(b_c)::value;
                 if (elect()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
-                        const uint64_t a = tc::sdesc_sw128(sQ + wg * Cfg::kTile + (k >> 2) * 16384) + (uint64_t)((k & 3) * 2);
-                        const uint64_t d = tc::sdesc_sw128(sK + b * Cfg::kTile + (k >> 2) * 16384) + (uint64_t)((k & 3) * 2);
+                        const uint64_t a = sdesc(Cfg::kAtQ + wg * Cfg::kTile + (k >> 2) * 16384 + (k & 3) * 32, 1);
+                        const uint64_t d = sdesc(Cfg::kAtK + b * Cfg::kTile + (k >> 2) * 16384 + (k & 3) * 32, 1);
                         tc::mma_ss(tmem + wg * 128, a, d, id_s, k > 0);
                     }
                     tc::commit(&bars.s_full[wg]);
                 }
                 __syncwarp();
             };
-            auto values = [&](int wg, int b, bool first) {
+            auto values = [&](auto wg_c, auto b_c, bool first) {
+                constexpr int wg = decltype(wg_c)::value, b = decltype(b_c)::value;
                 if (elect()) {
-                    const uint64_t d = sdesc_mn_sw128(sV + b * Cfg::kTile);
 #pragma unroll
                     for (int k = 0; k < kKeys / 16; ++k)
-                        tc::mma_ts(tmem + 256 + wg * D, tmem + wg * 128 + k * 8, d + (uint64_t)(k * 128), id_o, !first || k > 0);
+                        tc::mma_ts(tmem + 256 + wg * D, tmem + wg * 128 + k * 8, sdesc(Cfg::kAtV + b * Cfg::kTile + k * 2048, 1024), id_o, !first || k > 0);
                 }
                 __syncwarp();
             };
@@ -568,37 +591,44 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
             };
             for (;; ++n_item) {
                 const bool two = it.s.nq * p.G - it.qt * kR > kTileRows;
-                ok = wait(&bars.q_full, n_item & 1, abort_flag) && wait(&bars.k_full[g % kStages], (g / kStages) & 1, abort_flag);
-                if (ok) {
+                // scores of the item's first stage, in buffer b
+                auto start = [&](auto b_c) {
+                    constexpr int b = decltype(b_c)::value;
+                    if (!(ok = wait(&bars.q_full, n_item & 1, abort_flag) && wait(&bars.k_full[b], (g / kStages) & 1, abort_flag))) return;
                     tc::fence_after();
-                    scores(0, g % kStages);
-                    if (two) scores(1, g % kStages);
-                    done(&bars.k_empty[g % kStages]);
-                }
-                for (int st = st0; st < st1 && ok; ++st, ++g) {
-                    const int b = g % kStages, bn = (g + 1) % kStages;
-                    const bool more = st + 1 < st1;
+                    scores(c0, b_c);
+                    if (two) scores(c1, b_c);
+                    done(&bars.k_empty[b]);
+                };
+                // values of a stage in buffer b, scores of the next
+                auto step = [&](auto b_c, auto bn_c, bool first, bool more) {
+                    constexpr int b = decltype(b_c)::value, bn = decltype(bn_c)::value;
                     ok = wait(&bars.v_full[b], (g / kStages) & 1, abort_flag) && wait(&bars.p_full[0], gp[0] & 1, abort_flag);
-                    if (!ok) break;
+                    if (!ok) return;
                     ++gp[0];
                     tc::fence_after();
-                    values(0, b, st == st0);
+                    values(c0, b_c, first);
                     if (more) {
-                        if (!(ok = wait(&bars.k_full[bn], ((g + 1) / kStages) & 1, abort_flag))) break;
+                        if (!(ok = wait(&bars.k_full[bn], ((g + 1) / kStages) & 1, abort_flag))) return;
                         tc::fence_after();
-                        scores(0, bn);
+                        scores(c0, bn_c);
                     }
                     if (two) {
-                        if (!(ok = wait(&bars.p_full[1], gp[1] & 1, abort_flag))) break;
+                        if (!(ok = wait(&bars.p_full[1], gp[1] & 1, abort_flag))) return;
                         ++gp[1];
                         tc::fence_after();
-                        values(1, b, st == st0);
+                        values(c1, b_c, first);
                     }
                     done(&bars.v_empty[b]);
                     if (more) {
-                        if (two) scores(1, bn);
+                        if (two) scores(c1, bn_c);
                         done(&bars.k_empty[bn]);
                     }
+                };
+                if (g & 1) start(c1); else start(c0);
+                for (int st = st0; st < st1 && ok; ++st, ++g) {
+                    if (g & 1) step(c1, c0, st == st0, st + 1 < st1);
+                    else step(c0, c1, st == st0, st + 1 < st1);
                 }
                 done(&bars.o_full);
                 if (!ok) {
@@ -628,7 +658,7 @@ cudaError_t launch_one(const Attn &p, int *grid_out, cudaStream_t s) {
         return cudaFuncGetAttributes(&a, fn) == cudaSuccess && a.numRegs >= kRegsLaunch;
     }();
     if (!split_ok) return cudaErrorInvalidConfiguration;
-    constexpr size_t kBase = PromptCfg<D>::kSmem + 1024;
+    constexpr size_t kBase = PromptCfg<D>::kSmem + PromptCfg<D>::kAtQ - 1024;   // (what comes first: the system's 1 KB)
     const cudaError_t err = set_smem_once(fn, (int)kBase);
     if (err != cudaSuccess) return err;
     int grid = sm_count();
