@@ -101,6 +101,30 @@ __device__ inline bool elect() {
     return pred != 0;
 }
 
+// The products and their completion, by the threads whose `lead` is set (one of a
+// warp). Predicated, not branched around: in a branch of one lane the operands
+// cannot be formed in the uniform registers that the instructions take them from.
+__device__ inline void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ inline void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ inline void commit(uint32_t lead, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+        "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(lead)
+        : "memory");
+}
+
 template <int N>
 __device__ inline void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -562,33 +586,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
             static_assert(kStages == 2, "buffers");
             // Tile, stage and addresses are constants here: descriptors made from registers were kept
             // in too many of them, and moved to where the instructions take them from each time
-            // (the figure above: 766 -> 733 us).
+            // (the figure above: 766 -> 715 us).
+            const uint32_t lead = elect();
             auto scores = [&](auto wg_c, auto b_c) {
                 constexpr int wg = decltype(wg_c)::value, b = decltype(b_c)::value;
-                if (elect()) {
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint64_t a = sdesc(Cfg::kAtQ + wg * Cfg::kTile + (k >> 2) * 16384 + (k & 3) * 32, 1);
-                        const uint64_t d = sdesc(Cfg::kAtK + b * Cfg::kTile + (k >> 2) * 16384 + (k & 3) * 32, 1);
-                        tc::mma_ss(tmem + wg * 128, a, d, id_s, k > 0);
-                    }
-                    tc::commit(&bars.s_full[wg]);
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint64_t x = sdesc(Cfg::kAtQ + wg * Cfg::kTile + (k >> 2) * 16384 + (k & 3) * 32, 1);
+                    const uint64_t y = sdesc(Cfg::kAtK + b * Cfg::kTile + (k >> 2) * 16384 + (k & 3) * 32, 1);
+                    mma_ss(lead, tmem + wg * 128, x, y, id_s, k > 0);
                 }
-                __syncwarp();
+                commit(lead, &bars.s_full[wg]);
             };
             auto values = [&](auto wg_c, auto b_c, bool first) {
                 constexpr int wg = decltype(wg_c)::value, b = decltype(b_c)::value;
-                if (elect()) {
 #pragma unroll
-                    for (int k = 0; k < kKeys / 16; ++k)
-                        tc::mma_ts(tmem + 256 + wg * D, tmem + wg * 128 + k * 8, sdesc(Cfg::kAtV + b * Cfg::kTile + k * 2048, 1024), id_o, !first || k > 0);
-                }
-                __syncwarp();
+                for (int k = 0; k < kKeys / 16; ++k)
+                    mma_ts(lead, tmem + 256 + wg * D, tmem + wg * 128 + k * 8, sdesc(Cfg::kAtV + b * Cfg::kTile + k * 2048, 1024), id_o, !first || k > 0);
             };
-            auto done = [&](uint64_t *bar) {
-                if (elect()) tc::commit(bar);
-                __syncwarp();
-            };
+            auto done = [&](uint64_t *bar) { commit(lead, bar); };
             for (;; ++n_item) {
                 const bool two = it.s.nq * p.G - it.qt * kR > kTileRows;
                 // scores of the item's first stage, in buffer b
