@@ -316,13 +316,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
             float c_row = 0.f, l0 = 0.f, l1 = 0.f;
             int lim = 0;
             {
+                // whole rows at a time into the warp's part of the tile, then each thread its own
+                constexpr int kPieces = D / 8, kAtOnce = 32 / kPieces;
+                const long long at = (long long)(it.s.q0 + qi) * p.qs.token + (long long)head * p.qs.head;
+                const bool there = r < rows;
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    const int row = i * kAtOnce + lane / kPieces, piece = lane % kPieces;
+                    const long long src = __shfl_sync(0xffffffffu, there ? at : -1, row);
+                    copy16(chunk_at<D>(sQ + wg * Cfg::kTile, (r & 96) + row, piece), p.q + (src < 0 ? 0 : src) + piece * 8, src >= 0);
+                }
+                copies_commit();
+                copies_wait<0>();
+                __syncwarp();
                 uint4 x[D / 8];
                 uint32_t big = 0;
-                const bool there = r < rows;
-                const uint16_t *src = p.q + (size_t)(it.s.q0 + qi) * p.qs.token + (size_t)head * p.qs.head;
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) {
-                    x[i] = there ? *reinterpret_cast<const uint4 *>(src + i * 8) : make_uint4(0, 0, 0, 0);
+                    x[i] = lds_v4(chunk_at<D>(sQ + wg * Cfg::kTile, r & 127, i));
                     const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) big = max(big, max(w[j] & 0x7FFFu, w[j] >> 16 & 0x7FFFu));
@@ -418,27 +429,47 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
             float *part = p.part + (size_t)(c * 2 + (st0 == 0)) * part_floats(kR, D);
             const float l = l0 + l1;
             if (ok && mine) {
+                // 128 bytes of each of the warp's rows at a time through its part of the query tile (no
+                // product reads it any more), so that 8 lanes write a row
                 const float inv = l == 0.f ? 0.f : 1.f / l, up = pow2_biased(F);
-                uint16_t *dst = p.out + (size_t)(it.s.q0 + qi) * p.os.token + (size_t)head * p.os.head;
+                const long long at = (long long)(it.s.q0 + qi) * p.os.token + (long long)head * p.os.head;
+                uint8_t *const mid = sQ + wg * Cfg::kTile + (warp & 3) * 4096;
+                auto put = [&](int chunk, uint4 v) { *reinterpret_cast<uint4 *>(mid + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = v; };
+                auto rows_out = [&](auto &&store) {
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int row = k * 4 + (lane >> 3);
+                        store(row, lane & 7, lds_v4(mid + row * 128 + (((lane & 7) ^ (row & 7)) << 4)));
+                    }
+                    __syncwarp();
+                };
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
                     float o[32];
                     ld32(tO + i * 32, o);
                     wait_ld(o);
-                    if (r < rows) {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            const float v[8] = {o[j], o[j + 2], o[j + 4], o[j + 6], o[j + 1], o[j + 3], o[j + 5], o[j + 7]};
-                            if (whole) {
-                                *reinterpret_cast<uint4 *>(dst + i * 32 + j) =
-                                    make_uint4(bf16x2_of(v[0] * inv * up, v[1] * inv * up), bf16x2_of(v[2] * inv * up, v[3] * inv * up),
-                                               bf16x2_of(v[4] * inv * up, v[5] * inv * up), bf16x2_of(v[6] * inv * up, v[7] * inv * up));
-                            } else {
-                                float4 *d = reinterpret_cast<float4 *>(part + 2 * kR + 4 + r * D + i * 32 + j);
-                                d[0] = make_float4(v[0], v[1], v[2], v[3]);
-                                d[1] = make_float4(v[4], v[5], v[6], v[7]);
-                            }
+                    for (int j = 0; j < 32; j += 8) {
+                        const float v[8] = {o[j], o[j + 2], o[j + 4], o[j + 6], o[j + 1], o[j + 3], o[j + 5], o[j + 7]};
+                        if (whole) {
+                            put((i & 1) * 4 + j / 8, make_uint4(bf16x2_of(v[0] * inv * up, v[1] * inv * up), bf16x2_of(v[2] * inv * up, v[3] * inv * up),
+                                                                bf16x2_of(v[4] * inv * up, v[5] * inv * up), bf16x2_of(v[6] * inv * up, v[7] * inv * up)));
+                        } else {
+                            put(j / 4, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
+                            put(j / 4 + 1, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
                         }
+                    }
+                    if (!whole) {
+                        rows_out([&](int row, int piece, uint4 v) {
+                            const int y = (r & ~31) + row;
+                            if (y < rows) *reinterpret_cast<uint4 *>(part + 2 * kR + 4 + y * D + i * 32 + piece * 4) = v;
+                        });
+                    } else if (i & 1) {
+                        rows_out([&](int row, int piece, uint4 v) {
+                            const long long dst = __shfl_sync(0xffffffffu, at, row);
+                            if ((r & ~31) + row < rows) *reinterpret_cast<uint4 *>(p.out + dst + (i >> 1) * 64 + piece * 8) = v;
+                        });
                     }
                 }
                 if (r < rows) {
