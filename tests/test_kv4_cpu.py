@@ -58,7 +58,8 @@ def _append(L, c=None, **over):
 
 CACHES = [(dict(D=96), UNSUPPORTED), (dict(D=256), UNSUPPORTED), (dict(page_size=8), UNSUPPORTED), (dict(page_size=48), UNSUPPORTED),
           (dict(page_size=2048), UNSUPPORTED), (dict(n_pages=0), INVALID), (dict(Hkv=0), INVALID), (dict(k_codes=None), INVALID),
-          (dict(v_scales=A + 2), INVALID), (dict(n_pages=1 << 27), UNSUPPORTED), (dict(Hkv=2000), UNSUPPORTED)]
+          (dict(v_scales=A + 2), INVALID), (dict(n_pages=1 << 27), UNSUPPORTED), (dict(Hkv=2000), UNSUPPORTED),
+          (dict(n_pages=1 << 20, page_size=1024, Hkv=4), UNSUPPORTED)]
 
 
 @pytest.mark.parametrize("over,status", CACHES)
