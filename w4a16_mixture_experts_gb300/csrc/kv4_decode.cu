@@ -104,20 +104,6 @@ __device__ inline void bar_pass(int warp) {
     else asm volatile("barrier.cta.arrive 1, 128;" ::: "memory");
 }
 
-__device__ inline bool elect() {
-    uint32_t pred;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(pred));
-    return pred != 0;
-}
-
-// kind::f8f6f4 (e4m3 both), A from tensor memory.
-__device__ inline void mma_e4m3(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
 __device__ inline uint32_t idesc(int N, bool mn_major) {   // f32 sums; format 0 is f16 or e4m3, by the kind
     return (1u << 4) | (mn_major ? 3u << 15 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
@@ -342,14 +328,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
         }
     };
     const uint64_t desc_q = tc::sdesc_sw128(sQ), desc_v = v_desc<D>(sV), desc_p = p_desc<R>(sP);
-    auto issue_scores = [&]() {
-        if (elect()) {   // (warp 0)
+    const uint32_t lead = elect();
+    auto issue_scores = [&]() {   // (warp 0)
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k)
-                mma_e4m3(tcol + Cfg::kColS, tcol + k * 8, desc_q + (uint64_t)(k * 2), idesc(Cfg::kNS, false), k > 0);
-            tc::commit(&sh.s_full);
-        }
-        __syncwarp();
+        for (int k = 0; k < D / 32; ++k)
+            mma_e4m3(lead, tcol + Cfg::kColS, tcol + k * 8, desc_q + (uint64_t)(k * 2), idesc(Cfg::kNS, false), k > 0);
+        commit(lead, &sh.s_full);
     };
     // The first copies of an item (K and scales of its first unit, and V's, in no group
     // yet) and its queries are begun before what else the item's start or the last one's
@@ -593,14 +577,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
                 __syncthreads();
             }
             tc::fence_after();
-            if (warp == 1 && elect()) {
+            if (warp == 1) {
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k)
-                    tc::mma_ss(tcol + Cfg::kColO, desc_v + (uint64_t)(k * 128), desc_p + (uint64_t)(p_at / 16 + k * 16), idesc(Cfg::kNP, true),
-                               turn > 0 || k > 0);
-                tc::commit(&sh.o_full);
+                    mma_ss(lead, tcol + Cfg::kColO, desc_v + (uint64_t)(k * 128), desc_p + (uint64_t)(p_at / 16 + k * 16), idesc(Cfg::kNP, true),
+                           turn > 0 || k > 0);
+                commit(lead, &sh.o_full);
             }
-            __syncwarp();
         }
         copies_wait<0>();
         if (st < st1) {   // (cut short; the products in flight get a bounded wait)
