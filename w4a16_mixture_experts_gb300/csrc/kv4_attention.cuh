@@ -22,6 +22,7 @@ namespace kv4 {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMaxSeqs = 4096;       // of a call
 constexpr float kNoMax = -3e38f;   // below every score: nothing seen yet
 
 // Up to so many rows of a sequence share one streaming pass; more go to the
@@ -125,23 +126,45 @@ __device__ inline int tile_units(const Seq &s, int G, int R, int qt) {
     return max(1, (tile_keys(s, G, R, qt) + kKeys - 1) / kKeys);
 }
 
-// The units of one head of a sequence, leading ones included. A whole warp calls
-// it, each lane with a sequence of its own (many row tiles: all lanes together).
+// The units of a sequence's row tiles, leading ones included, by a whole warp for
+// one sequence.
 template <int kKeys, int kLead>
-__device__ long long head_units(const Attn &p, const Seq &s, int R) {
-    const int tiles = (s.nq * p.G + R - 1) / R, lane = threadIdx.x & 31;
+__device__ long long tiles_units(const Seq &s, int G, int R) {
+    const int tiles = (s.nq * G + R - 1) / R;
+    long long m = 0;
+    for (int qt = threadIdx.x & 31; qt < tiles; qt += 32) m += tile_units<kKeys>(s, G, R, qt) + kLead;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) m += __shfl_xor_sync(0xffffffffu, m, x);
+    return m;
+}
+
+// The units of one head of each thread's sequence. Sequences of more than two row
+// tiles take a warp each: in a CTA of several warpgroups they are shared out over
+// all warps through `mid` (12 prompts of up to 1500 queries: 99.2 us with one warp for
+// them, 98.0 so).
+template <int kThreads, int kKeys, int kLead>
+__device__ long long head_units(const Attn &p, const Seq &s, int R, long long *mid) {
+    const int tiles = (s.nq * p.G + R - 1) / R, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long n = 0;
     if (tiles <= 2)
         for (int qt = 0; qt < tiles; ++qt) n += tile_units<kKeys>(s, p.G, R, qt) + kLead;
-    for (uint32_t many = __ballot_sync(0xffffffffu, tiles > 2); many; many &= many - 1) {
-        const int src = __ffs(many) - 1;
-        const Seq o{0, __shfl_sync(0xffffffffu, s.nq, src), __shfl_sync(0xffffffffu, s.len, src)};
-        const int ot = (o.nq * p.G + R - 1) / R;
-        long long m = 0;
-        for (int qt = lane; qt < ot; qt += 32) m += tile_units<kKeys>(o, p.G, R, qt) + kLead;
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) m += __shfl_xor_sync(0xffffffffu, m, x);
-        if (lane == src) n = m;
+    if (kThreads <= 128) {
+        for (uint32_t many = __ballot_sync(0xffffffffu, tiles > 2); many; many &= many - 1) {
+            const int src = __ffs(many) - 1;
+            const long long m = tiles_units<kKeys, kLead>(Seq{0, __shfl_sync(0xffffffffu, s.nq, src), __shfl_sync(0xffffffffu, s.len, src)}, p.G, R);
+            if (lane == src) n = m;
+        }
+    } else if (__syncthreads_or(tiles > 2)) {
+        mid[threadIdx.x] = tiles > 2 ? (long long)s.nq << 32 | (long long)s.len : -1;
+        __syncthreads();
+        for (int i = warp; i < kThreads; i += kThreads / 32) {
+            const long long x = mid[i];
+            if (x < 0) continue;
+            const long long m = tiles_units<kKeys, kLead>(Seq{0, (int)(x >> 32), (int)x}, p.G, R);
+            if (lane == 0) mid[i] = m;
+        }
+        __syncthreads();
+        if (tiles > 2) n = mid[threadIdx.x];
     }
     return n;
 }
@@ -203,7 +226,7 @@ __device__ Shares first_item(const Attn &p, int R, int c, int *pre, long long *w
     for (int b0 = 0; b0 < p.b.B; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
         s = b < p.b.B ? seq_of(p.b, b, p.ctrl) : Seq{0, 0, 0};
-        per_head = head_units<kKeys, kLead>(p, s, R);
+        per_head = head_units<kThreads, kKeys, kLead>(p, s, R, reinterpret_cast<long long *>(pre + kMaxSeqs));
         n = per_head * p.c.Hkv;
         long long inc = n;
 #pragma unroll

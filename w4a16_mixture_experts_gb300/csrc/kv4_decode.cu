@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
     DecodeShared<R> &sh = *reinterpret_cast<DecodeShared<R> *>(s_dyn + Cfg::kSmem);
     // the sequences' prefix: needed only before the first operand is written
     int *const s_pre = reinterpret_cast<int *>(sV);
-    static_assert(sizeof(int) * 4097 <= (size_t)(Cfg::kV + Cfg::kPs * Cfg::kP), "prefix");
+    static_assert(sizeof(int) * (kMaxSeqs + 1) <= (size_t)(Cfg::kV + Cfg::kPs * Cfg::kP), "prefix");
 
     if (tid == 0) {
         mbar_init(&sh.s_full, 1);
