@@ -8,6 +8,7 @@
 
 #include "common.cuh"
 #include "kernels.cuh"
+#include "kv4_kernels.cuh"
 #include "w4a16moe.h"
 
 namespace moe {

@@ -11,7 +11,7 @@
 #pragma once
 
 #include "common.cuh"
-#include "kernels.cuh"
+#include "kv4_kernels.cuh"
 
 namespace moe {
 namespace kv4 {
