@@ -458,13 +458,13 @@ def kv4_workspace(T: int = 0, Hq: int = 1, Hkv: int = 1, D: int = 128, device=No
     return torch.zeros(n, dtype=torch.uint8, device=device if device is not None else "cuda")
 
 
-_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+_BF16, _I32, _F32, _Tensor = torch.bfloat16, torch.int32, torch.float32, torch.Tensor
 _strides = {}   # (token, head) -> the struct: few pairs occur, and forming one costs more than finding it
 
 
 def _heads(t, name, T=None, heads=None, D=None):
-    """The strides of a bf16 [T, heads, D] CUDA tensor with contiguous D."""
-    if not isinstance(t, torch.Tensor):
+    """The strides, and the shape, of a bf16 [T, heads, D] CUDA tensor with contiguous D."""
+    if type(t) is not _Tensor and not isinstance(t, _Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     shape = t.shape
     if t.dtype != _BF16 or len(shape) != 3 or (T is not None and shape[0] != T) or (
@@ -482,15 +482,16 @@ def _heads(t, name, T=None, heads=None, D=None):
         if len(_strides) > 4096:
             _strides.clear()
         st = _strides[key] = moe_strides(*key)
-    return st
+    return st, shape
 
 
 def _vec(t, name, dtype, n=None):
-    if not isinstance(t, torch.Tensor):
+    if type(t) is not _Tensor and not isinstance(t, _Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.dtype != dtype or t.dim() != 1 or (n is not None and t.shape[0] != n) or not t.is_cuda or not t.is_contiguous():
+    shape = t.shape
+    if t.dtype != dtype or len(shape) != 1 or (n is not None and shape[0] != n) or not t.is_cuda or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s CUDA tensor%s, got %s %s"
-                         % (name, dtype, "" if n is None else " of %d values" % n, t.dtype, tuple(t.shape)))
+                         % (name, dtype, "" if n is None else " of %d values" % n, t.dtype, tuple(shape)))
     return t.data_ptr()
 
 
@@ -508,15 +509,13 @@ def moe_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, ep
     positions int32 [T], inv_freq f32 [rot/2] (both None: norms alone), weights bf16 [D] or None.
     The pairs are (i, i + rot/2), or (2i, 2i + 1) with interleaved. Returns (q_out, k_out).
     """
-    qs = _heads(q, "q")
-    T, Hq, D = q.shape
-    ks = _heads(k, "k", T, None, D)
-    Hkv = k.shape[1]
+    qs, (T, Hq, D) = _heads(q, "q")
+    ks, (_, Hkv, _) = _heads(k, "k", T, None, D)
     if q_out is None:
         q_out = torch.empty(T, Hq, D, dtype=_BF16, device=q.device)
     if k_out is None:
         k_out = torch.empty(T, Hkv, D, dtype=_BF16, device=q.device)
-    qos, kos = _heads(q_out, "q_out", T, Hq, D), _heads(k_out, "k_out", T, Hkv, D)
+    qos, kos = _heads(q_out, "q_out", T, Hq, D)[0], _heads(k_out, "k_out", T, Hkv, D)[0]
     pos = fr = None
     rot = 0
     if inv_freq is not None:
@@ -535,9 +534,8 @@ def moe_kv4_append(k, v, slots, cache: Kv4Cache, ws=None, stream=None):
     slots[t] (int32 [T]; -1: not stored). ws: kv4_workspace(), whose error word
     moe_check_device_error reads. Returns the cache."""
     c, Hkv, D = _cache(cache)
-    ks = _heads(k, "k", None, Hkv, D)
-    T = k.shape[0]
-    vs = _heads(v, "v", T, Hkv, D)
+    ks, (T, _, _) = _heads(k, "k", None, Hkv, D)
+    vs = _heads(v, "v", T, Hkv, D)[0]
     if ws is None:
         ws = kv4_workspace(device=k.device)
     _check(lib().moe_kv4_append(k.data_ptr(), ks, v.data_ptr(), vs, _vec(slots, "slots", torch.int32, T), T, c,
@@ -575,8 +573,7 @@ def moe_kv4_attention(q, cache: Kv4Cache, page_table, lens, cu_q=None, max_q: in
     ws: kv4_workspace(T, Hq, Hkv, D). Returns out, or (out, lse f32 [T, Hq]) where lse is given
     (a tensor, or True to have it made)."""
     c, Hkv, D = _cache(cache)
-    qs = _heads(q, "q", None, None, D)
-    T, Hq = q.shape[0], q.shape[1]
+    qs, (T, Hq, _) = _heads(q, "q", None, None, D)
     B = lens.shape[0]
     at = _vec(lens, "lens", torch.int32)
     cu = None if cu_q is None else _vec(cu_q, "cu_q", torch.int32, B + 1)
@@ -585,7 +582,7 @@ def moe_kv4_attention(q, cache: Kv4Cache, page_table, lens, cu_q=None, max_q: in
         raise ValueError("page_table must have a row for each of the %d sequences, got %s" % (B, tuple(page_table.shape)))
     if out is None:
         out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device)
-    os_ = _heads(out, "out", T, Hq, D)
+    os_ = _heads(out, "out", T, Hq, D)[0]
     if lse is True:
         lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
     if lse is not None:
