@@ -214,10 +214,11 @@ __device__ inline void add2(float &a, float &b, float c) {
         : "+f"(a), "+f"(b)
         : "f"(c));
 }
-__device__ inline void mul2(float &a, float &b, float c) {
-    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+__device__ inline void fma2(float &a, float &b, float c, float d) {   // (a, b) = (a, b) * c + d
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
         : "+f"(a), "+f"(b)
-        : "f"(c));
+        : "f"(c), "f"(d));
 }
 
 template <int D, int kAt>
@@ -268,9 +269,9 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(Rows p) {
             // rint(x / s) from x times the approximate reciprocal, which is within 4e-6 of the
             // quotient (|x / s| is at most 7.03). Quotients of 8-bit mantissas are halves exactly,
             // as often as not in a warp's 256, or at least 1 / 1020 away from one; so the product
-            // is first rounded to 2^-11, which makes halves of those and takes no other across.
-            // Adding 1.5 2^23 + 8 then rounds to whole numbers, ties to even, and leaves the code
-            // in the low bits. A scale near the subnormals, which may round far, takes the
+            // is first rounded to 2^-11 (by adding 1.5 2^12), which makes halves of those and takes
+            // no other across. Adding 1.5 2^23 + 8 less that then rounds to whole numbers, ties to
+            // even, and leaves the code in the low bits. A scale near the subnormals, which may round far, takes the
             // division and a clamp.
             constexpr float kGrid = 6144.f, kWhole = 12582920.f;   // 1.5 2^12, 1.5 2^23 + 8
             constexpr uint32_t kBits = 0x4B400000u;                // of 1.5 2^23
@@ -283,10 +284,8 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(Rows p) {
                 if (s > 1e-37f) {
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) {
-                        mul2(x[i], x[i + 1], inv);
-                        add2(x[i], x[i + 1], kGrid);
-                        add2(x[i], x[i + 1], -kGrid);
-                        add2(x[i], x[i + 1], kWhole);
+                        fma2(x[i], x[i + 1], inv, kGrid);
+                        add2(x[i], x[i + 1], kWhole - kGrid);
                         word += __float_as_uint(x[i]) << (4 * i);
                         word += __float_as_uint(x[i + 1]) << (4 * i + 4);
                     }
