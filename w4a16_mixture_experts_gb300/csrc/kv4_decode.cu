@@ -42,7 +42,11 @@ namespace {
 using namespace kv4;
 
 constexpr int kKeys = 128;   // keys of a unit: a warpgroup's turn
-constexpr int kLead = 2;     // an item's start and end take about 9000 clocks, a unit 3900
+// What an item's start and end count for, in units (96 sequences of 400 to 4001 keys, D = 128: 43.9,
+// 41.8, 40.4, 40.9 us with 1, 2, 3, 4; 24 of 833 to 2777 keys, 16 rows, D = 64: 26.8, 26.5, 25.0, 26.0
+// with 2, 3, 4, 6).
+template <int D>
+constexpr int kLead = D == 128 ? 3 : 4;
 constexpr uint32_t kNibs = 0x0F0F0F0Fu;
 
 template <int D, int R>
@@ -237,7 +241,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
     }
     const int c = blockIdx.x;
     Item it;
-    const Shares shares = first_item<Cfg::kThreads, kKeys, kLead>(p, R, c, s_pre, sh.sums, sh.first, it);
+    const Shares shares = first_item<Cfg::kThreads, kKeys, kLead<D>>(p, R, c, s_pre, sh.sums, sh.first, it);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -246,8 +250,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
     const int u_end = c < shares.C ? shares.begin(c + 1) : 0;
     int st0 = 0, st1 = 0;
     if (c < shares.C) {
-        st0 = max(shares.begin(c) - it.first - kLead, 0);
-        st1 = min(it.units, u_end - it.first - kLead);
+        st0 = max(shares.begin(c) - it.first - kLead<D>, 0);
+        st1 = min(it.units, u_end - it.first - kLead<D>);
     }
     if (st1 <= st0) {   // (a share that ends among leading units has nothing to do)
         if (tid == 0) p.begun[c].last = 0;
@@ -600,12 +604,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
         const bool first_part = st0 == 0, whole = first_part && st1 == it.units;
         bool last_item = it.first + it.span >= u_end;
         if (!last_item) {
-            next_item<kKeys, kLead>(p, R, it);
-            last_item = u_end - it.first <= kLead;
+            next_item<kKeys, kLead<D>>(p, R, it);
+            last_item = u_end - it.first <= kLead<D>;
         }
         if (!last_item) {
             st0 = 0;
-            st1 = min(it.units, u_end - it.first - kLead);
+            st1 = min(it.units, u_end - it.first - kLead<D>);
             page0 = page_of(0);
             page1 = page_of(1);
         }
