@@ -54,10 +54,9 @@ constexpr int kStages = 2;
 // registers a thread after the split: 256 x 160 + 256 x 64 + 128 x 32 = 640 x 96
 constexpr int kRegsSoft = 160, kRegsDeq = 64, kRegsMma = 32, kRegsLaunch = 96;
 static_assert(256 * kRegsSoft + 256 * kRegsDeq + 128 * kRegsMma <= kThreads * kRegsLaunch, "register split");
-// What an item's start and end count for, in stages. (Ragged prompts, D = 64: 103.9 us
-// with 2, 97.2 with 3, 98.0 with 4.)
-template <int D>
-constexpr int kLead = D == 128 ? 2 : 3;
+// What an item's start and end count for, in stages. (Ragged prompts, D = 64: 103.9 us with 2, 97.2
+// with 3, 98.0 with 4; the chunk of 4096, D = 128: 700.0, 697.0, 695.4.)
+constexpr int kLead = 3;
 
 template <int D>
 struct PromptCfg {
@@ -243,12 +242,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
     pdl_launch_dependents();
     const int c = blockIdx.x;
     Item it;
-    const Shares shares = first_item<kThreads, kKeys, kLead<D>>(p, kR, c, s_pre, s_sums, s_first, it);
+    const Shares shares = first_item<kThreads, kKeys, kLead>(p, kR, c, s_pre, s_sums, s_first, it);
     const int u_begin = c < shares.C ? shares.begin(c) : 0, u_end = c < shares.C ? shares.begin(c + 1) : 0;
     // the stages of an item in this CTA's share: [st0, st1)
     auto stages_of = [&](const Item &x, int &st0, int &st1) {
-        st0 = max(u_begin - x.first - kLead<D>, 0);
-        st1 = min(x.units, u_end - x.first - kLead<D>);
+        st0 = max(u_begin - x.first - kLead, 0);
+        st1 = min(x.units, u_end - x.first - kLead);
         return st1 > st0;
     };
     int st0, st1;
@@ -259,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
     // the next item with stages in the share; false: there is none
     auto go_on = [&]() {
         if (it.first + it.span >= u_end) return false;
-        next_item<kKeys, kLead<D>>(p, kR, it);
+        next_item<kKeys, kLead>(p, kR, it);
         return stages_of(it, st0, st1);
     };
     if (warp == kWMma) {
