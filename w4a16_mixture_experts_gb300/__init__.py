@@ -467,16 +467,19 @@ def _heads(t, name, T=None, heads=None, D=None):
     if type(t) is not _Tensor and not isinstance(t, _Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     shape = t.shape
-    if t.dtype != _BF16 or len(shape) != 3 or (T is not None and shape[0] != T) or (
-            heads is not None and shape[1] != heads) or (D is not None and shape[2] != D):
+    good = t.dtype is _BF16 and len(shape) == 3
+    if good:
+        n, h, d = shape
+        good = (T is None or n == T) and (heads is None or h == heads) and (D is None or d == D)
+    if not good:
         raise ValueError("%s must be bf16 [%s, %s, %s], got %s %s" % (
             name, "T" if T is None else T, "heads" if heads is None else heads, "D" if D is None else D, t.dtype,
             tuple(shape)))
     token, head, one = t.stride()
-    if not t.is_cuda or (one != 1 and shape[2] > 1):
+    if not t.is_cuda or (one != 1 and d > 1):
         raise ValueError("%s must be a CUDA tensor with contiguous head values" % name)
     # (a dimension of one entry has no stride that matters)
-    key = (token if shape[0] > 1 else 0, head if shape[1] > 1 else 0)
+    key = (token if n > 1 else 0, head if h > 1 else 0)
     st = _strides.get(key)
     if st is None:
         if len(_strides) > 4096:
@@ -489,7 +492,7 @@ def _vec(t, name, dtype, n=None):
     if type(t) is not _Tensor and not isinstance(t, _Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     shape = t.shape
-    if t.dtype != dtype or len(shape) != 1 or (n is not None and shape[0] != n) or not t.is_cuda or not t.is_contiguous():
+    if t.dtype is not dtype or (len(shape) != 1 if n is None else shape != (n,)) or not t.is_cuda or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s CUDA tensor%s, got %s %s"
                          % (name, dtype, "" if n is None else " of %d values" % n, t.dtype, tuple(shape)))
     return t.data_ptr()
