@@ -62,18 +62,8 @@ struct Attn {
 // its values, and the rows' values.
 __host__ __device__ constexpr int part_floats(int R, int D) { return 2 * R + 4 + R * D; }
 
-// Loads of the cache that stay where they are written (the compiler would move
-// them down to their first use, and their latency with them), past the L1.
-__device__ inline uint4 ld_stream(const void *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
-}
-__device__ inline uint16_t ld_here(const uint16_t *p) {
-    uint16_t v;
-    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
-    return v;
-}
+// A load that stays where it is written (the compiler would move it down to its
+// first use, and its latency with it).
 __device__ inline int ld_here(const int32_t *p) {
     int v;
     asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(v) : "l"(p));

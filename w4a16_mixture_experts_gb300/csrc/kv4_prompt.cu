@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
         uint32_t size;
         asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(size));
         if (smem_u32(s_dyn) > Cfg::kAtQ || smem_u32(s_dyn) + size < Cfg::kAtQ + Cfg::kSmem) {   // (the whole card: the same for every CTA)
+            pdl_wait();
             if (threadIdx.x == 0) {
                 set_error(p.ctrl, MOE_ERR_DEVICE);
                 p.begun[blockIdx.x].last = 0;
