@@ -562,7 +562,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
                     up[r] = turn > 0 ? fmaxf(x, 0.f) : x == kNoMax ? 0.f : x;
                     if (tid == r) sh.m[r] += up[r];   // (all have read the old maxima before the barriers)
                     s[r] -= up[r];
-                    up[r] = exp2_approx(-up[r]);
+                    // (turn 0: nothing to rescale, and a maximum far below zero has no power of two)
+                    up[r] = turn > 0 ? exp2_approx(-up[r]) : 1.f;
                     l[r] *= up[r];
                 }
                 if (turn > 0) {
