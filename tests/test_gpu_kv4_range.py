@@ -2,6 +2,8 @@
 
 Tolerances are those that test_gpu_kv4.py derives.
 """
+import math
+
 import pytest
 import torch
 
@@ -73,3 +75,21 @@ def test_keys_far_below_zero_beside_others(nq):
     q[..., 0] = -150 / 3.5 * D ** 0.5
     for max_q in (nq, 1, 4096):
         _check(q, cache, table, [n], [nq], max_q=max_q)
+
+
+# ---- queries that are not finite, and no key --------------------------------------------------------------------
+
+@pytest.mark.parametrize("nq", [6, 140])
+def test_queries_that_are_not_finite_and_see_nothing(nq):
+    g = _gen(nq)
+    n, G = 3, 4
+    cache, table, _, _ = _one_sequence(g, n, 16, 128, Hkv=2)
+    q = _randn(g, nq, 2 * G, 128).bfloat16()
+    q[0, 1, 5], q[1, 7, 0], q[nq - n - 1, 2, 127] = float("nan"), float("inf"), -float("inf")
+    q[nq - 1, 3, 9] = float("nan")                       # this one sees keys
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    for max_q in (1, nq, 4096):
+        out, lse = moe.moe_kv4_attention(q, cache, table, i32(n), cu_q=i32(0, nq), max_q=max_q, lse=True)
+        assert (out[:nq - n] == 0).all() and (lse[:nq - n] == -math.inf).all()
+        assert out[nq - 1, 3].isnan().all() and lse[nq - 1, 3].isnan()
+        assert out[nq - 1, [0, 1, 2, 4, 5, 6, 7]].isfinite().all()

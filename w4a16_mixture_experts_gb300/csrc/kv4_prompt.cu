@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                 if (p.scale < 0.f) f = -f;   // so that the largest product is the largest score
                 if (there) lim = it.s.len - it.s.nq + qi + 1;
                 c_row = fabsf(p.scale) * kLog2e * pow2_biased(e);
-                if (big >= 0x7F80u) l0 = __uint_as_float(0x7fc00000u);   // a query that is not finite: NaN
+                if (big >= 0x7F80u && lim > 0) l0 = __uint_as_float(0x7fc00000u);   // a query that is not finite: NaN, where it sees a key
                 uint8_t *const tile = sQ + wg * Cfg::kTile;
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) {
