@@ -1,6 +1,8 @@
-"""Attention over the 4-bit cache where values lie far apart: scores far below zero.
+"""Attention over the 4-bit cache where values lie far apart: scores far below zero, queries with one value far above
+the rest.
 
-Tolerances are those that test_gpu_kv4.py derives.
+Tolerances are those that test_gpu_kv4.py derives, key by key: a score's error goes with its own key's products. A query
+value keeps 2^-33 of the row's largest at least (half a step of fp16's smallest, against a largest of 2^8).
 """
 import math
 
@@ -8,7 +10,7 @@ import pytest
 import torch
 
 import w4a16_mixture_experts_gb300 as moe
-from test_gpu_kv4 import _check, _filled, _gen, _randn, _tables
+from test_gpu_kv4 import U16, U32, UB, _check, _filled, _gen, _randn, _tables, _unpack
 
 pytestmark = pytest.mark.gpu
 
@@ -39,9 +41,52 @@ def _one_sequence(g, n, S, D, Hkv=1):
     return cache, table, table[0].long()[j // S], j % S
 
 
+def _near(q, cache, table, n, max_q, scale=None, floor=2.0 ** -21, rows=None, copies=1):
+    """Attention of the last queries of one sequence of n keys against 64 bits; rows: of the queries, which to compare.
+    copies: sequences that are all this one (on the same pages), so that a block has whole sequences and not a few keys."""
+    nq, Hq, D = q.shape
+    Hkv, S = cache.k_scales.shape[1:]
+    G = Hq // Hkv
+    scale = D ** -0.5 if scale is None else scale
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    ws = moe.kv4_workspace(copies * nq, Hq, Hkv, D)
+    cu = torch.arange(0, copies * nq + 1, nq, dtype=torch.int32, device="cuda")
+    out, lse = moe.moe_kv4_attention(q.repeat(copies, 1, 1), cache, table.repeat(copies, 1), i32(*[n] * copies), cu_q=cu, max_q=max_q,
+                                     scale=scale, lse=True, ws=ws)
+    assert moe.moe_check_device_error(ws) == 0
+    out, lse = out.view(copies, nq, Hq, D), lse.view(copies, nq, Hq)
+    shares = torch.cuda.get_device_properties(0).multi_processor_count if copies == 1 else 1   # that the keys are cut into, at least
+    adds = n / (16 * shares) + 4 * 128 / 16 + 640
+    pages = table[0, :-(-n // S)].long()
+    for h in range(Hkv):
+        vs = cache.v_scales[pages, h].reshape(-1)[:n].double()
+        codes = _unpack(cache.v_codes[pages, h], torch.ones_like(cache.v_scales[pages, h])).reshape(-1, D)[:n]
+        k = _unpack(cache.k_codes[pages, h], cache.k_scales[pages, h]).reshape(-1, D)[:n]
+        for i in range(nq) if rows is None else rows:
+            seen = n - nq + i + 1
+            assert seen > 0
+            x = q[i, h * G:(h + 1) * G].double()
+            s = scale * (x @ k[:seen].T)
+            z = torch.logsumexp(s, -1, keepdim=True)
+            p, ka = (s - z).exp(), k[:seen].abs()
+            ds = 2 * U32 * (D + 4) * abs(scale) * (x.abs() @ ka.T) + abs(scale) * 2.0 ** -33 * x.abs().amax(-1, keepdim=True) * ka.sum(-1)
+            ds = torch.expm1(2 * ds)
+            want = (p * vs[:seen]) @ codes[:seen]
+            absolute = codes[:seen].abs()
+            mass = (p * vs[:seen]) @ absolute
+            C = (p * vs[:seen]).amax(-1, keepdim=True)
+            dl = (p * ds).sum(-1, keepdim=True)
+            tol = UB * want.abs() + (U16 + dl + 2 * U32 * adds) * mass + (p * vs[:seen] * ds) @ absolute + floor * C * absolute.sum(0)
+            off = (out[:, i, h * G:(h + 1) * G].double() - want).abs()
+            assert (off <= tol).all(), (i, h, float((off - tol).max()), float((off / tol.clamp(min=1e-300)).max()))
+            off = (lse[:, i, h * G:(h + 1) * G].double() - z.squeeze(-1)).abs()
+            ltol = dl.squeeze(-1) + 2 * U32 * adds + 2 * U32 * z.squeeze(-1).abs()
+            assert (off <= ltol).all(), (i, h, float((off - ltol).max()))
+
+
 # ---- scores far below zero -----------------------------------------------------------------------------------
 
-@pytest.mark.parametrize("nats", [-100])
+@pytest.mark.parametrize("nats", [-100, -1000, -30000])
 @pytest.mark.parametrize("n", [1, 128, 3000])
 @pytest.mark.parametrize("nq,D", [(1, 128), (1, 64), (6, 128), (140, 64)])
 def test_scores_that_all_lie_far_below_zero(nats, n, nq, D):
@@ -93,3 +138,22 @@ def test_queries_that_are_not_finite_and_see_nothing(nq):
         assert (out[:nq - n] == 0).all() and (lse[:nq - n] == -math.inf).all()
         assert out[nq - 1, 3].isnan().all() and lse[nq - 1, 3].isnan()
         assert out[nq - 1, [0, 1, 2, 4, 5, 6, 7]].isfinite().all()
+
+
+# ---- queries with one value far above the rest -------------------------------------------------------------------
+
+@pytest.mark.parametrize("nq,max_q", [(1, 1), (1, 4096), (5, 1), (5, 5), (70, 1)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("above", [9, 11, 13, 17, 20])
+def test_queries_with_a_value_far_above_the_rest(nq, max_q, D, above):
+    """Where K holds zeros beside it, the rest alone decides."""
+    g = _gen(above + D)
+    n, S, G = 700, 16, 4
+    cache, table, page, at = _one_sequence(g, n, S, D)
+    for d in (4, 37):
+        codes = _unpack(cache.k_codes[page, 0, at], torch.ones(n, device="cuda"))
+        codes[:, d] = 0
+        cache.k_codes[page, 0, at] = _words(codes)
+    q = (1.6 * _randn(g, nq, G, D)).bfloat16()
+    q[..., 4], q[..., 37] = 2.0 ** above, -1.7 * 2.0 ** above
+    _near(q, cache, table, n, max_q)

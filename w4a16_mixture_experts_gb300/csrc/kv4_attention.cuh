@@ -340,14 +340,6 @@ __device__ inline void commit(uint32_t lead, uint64_t *bar) {
         "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(lead)
         : "memory");
 }
-// kind::f8f6f4 (e4m3 both), A from tensor memory.
-__device__ inline void mma_e4m3(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %4, 0;\n\t"
-        "@p tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, q;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
-        : "memory");
-}
 
 }  // namespace kv4
 }  // namespace moe

@@ -19,17 +19,15 @@
 // loaded from global memory) took 770 warp instructions for 32 keys at R = 8, for
 // shuffles of scales and maxima, address arithmetic and a transposition of P.
 //
-// K enters as e4m3: a code n = q + 8 in the low bits of an e4m3 byte is n 2^-9
-// exactly, on both sides of its smallest normal, so two ANDs and a shift make
-// operands of 8 codes. A query row enters as the sum of two e4m3 numbers (two
-// columns of the product), less its own exponent: 8 bits, all that a bf16 has,
-// but for values below 2^-9 of the row's largest, which are rounded at 2^-18 of
-// it. The 8 that each code has too many is taken off in fp32: -8 sum q.
-// V enters as fp16, exactly. A V scale multiplies its key's probabilities just
+// K and V enter as fp16 codes less 8, exactly, and a K scale multiplies its key's
+// scores in fp32. A query row enters as fp16 less its own exponent, its largest
+// value brought to [2^8, 2^9): exactly, but for values below 2^-25 of the largest,
+// which are rounded at 2^-33 of it. (With K as e4m3 codes q + 8, which take a third
+// of the instructions, and a query as two e4m3 numbers, what a value far above the
+// rest left of them was rounded at 2^-18 of it, and 8 times it passed through the
+// sums of keys that hold zeros beside it.) A V scale multiplies its key's probabilities just
 // before they are rounded to fp16, less the exponent F of the largest V scale so
-// far (a power of two, put back at the end), so that no range of scales is lost.
-#include <cuda_fp8.h>
-
+// far (a power of two, put back at the end).
 #include <type_traits>
 
 #include "kv4_attention.cuh"
@@ -47,19 +45,18 @@ constexpr int kKeys = 128;   // keys of a unit: a warpgroup's turn
 // with 2, 3, 4, 6).
 template <int D>
 constexpr int kLead = D == 128 ? 3 : 4;
-constexpr uint32_t kNibs = 0x0F0F0F0Fu;
 
 template <int D, int R>
 struct DecodeCfg {
     static constexpr int kThreads = 128;                  // a warpgroup
     static constexpr int kPerSm = R < 16 ? 4 : 3;         // CTAs an SM
-    static constexpr int kNS = 2 * R, kNP = R < 16 ? 16 : R;   // columns of S^T (two a row) and of O^T (R = 8: twice the same)
+    static constexpr int kNP = R < 16 ? 16 : R;           // columns of S^T and of O^T (R = 8: twice the same)
     static constexpr int kV = 128 * D * 2, kP = R * 256;  // bytes of the operands
     static constexpr int kPs = R < 32 ? 2 : 1;            // of P: two where they fit, one read while the next is written
-    static constexpr int kQ = kNS * 128;
+    static constexpr int kQ = R * D * 2;
     static constexpr int kWarpRaw = 32 * D / 2, kRaw = 4 * kWarpRaw;   // codes of a warp's 32 keys (K or V), of all
     // tensor memory: K's row, scores, values' sums
-    static constexpr int kColS = 32, kColO = kColS + kNS, kCols = R < 16 ? 64 : 128;
+    static constexpr int kColS = D / 2, kColO = kColS + kNP, kCols = kColO + kNP > 64 ? 128 : 64;
     static_assert(kColO + kNP <= kCols, "tensor memory");
     static constexpr int kSmem = kQ + kV + kPs * kP + 2 * kRaw;
     static constexpr int kChunks = D / 32;                // 16-byte pieces of a row of codes
@@ -67,7 +64,7 @@ struct DecodeCfg {
 
 template <int R>
 struct DecodeShared {
-    alignas(16) float c[R], base[R], m[R], wm[4][R];
+    alignas(16) float c[R], m[R], wm[4][R];
     alignas(16) uint16_t scales[4][3][2][32];   // of a warp's units in turn: K's, V's
     uint64_t s_full, o_full;                    // scores formed, values added
     long long sums[4];
@@ -108,7 +105,7 @@ __device__ inline void bar_pass(int warp) {
     else asm volatile("barrier.cta.arrive 1, 128;" ::: "memory");
 }
 
-__device__ inline uint32_t idesc(int N, bool mn_major) {   // f32 sums; format 0 is f16 or e4m3, by the kind
+__device__ inline uint32_t idesc(int N, bool mn_major) {   // f16 operands, f32 sums
     return (1u << 4) | (mn_major ? 3u << 15 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
@@ -127,8 +124,13 @@ __device__ inline uint64_t p_desc(const void *p) {
     return (uint64_t)((smem_u32(p) >> 4) & 0x3FFFu) | (uint64_t)(128u >> 4) << 16 | (uint64_t)(R > 8 ? 2048u >> 4 : 0u) << 32 | (uint64_t)1u << 46;
 }
 
-__device__ inline uint32_t e4m3_of(float x) { return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3); }
-__device__ inline float of_e4m3(uint32_t b) { return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b, __NV_E4M3))); }
+// Q: rows of 128 swizzled bytes (64 values), 8 rows an atom of 1024, the next 8 rows
+// behind it (8 rows only: the same again).
+template <int R>
+__device__ inline uint64_t q_desc(const void *p) {
+    return (uint64_t)((smem_u32(p) >> 4) & 0x3FFFu) | (uint64_t)1u << 16 | (uint64_t)(R > 8 ? 1024u >> 4 : 0u) << 32 | (uint64_t)1u << 46 |
+           (uint64_t)2u << 61;
+}
 
 __device__ inline uint32_t half2_of(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
@@ -306,14 +308,22 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
 #pragma unroll
         for (int i = 0; i < Cfg::kChunks; ++i) w[i] = lds_v4(raw + (lane * Cfg::kChunks + (i ^ turned(lane))) * 16);
     };
-    auto write_k = [&]() {   // codes 0, 2, 4, 6 of a word are one column, 1, 3, 5, 7 the next
+    auto write_k = [&]() {   // the pairs (k, k + 4) of a word's codes, a column each
         uint4 w[Cfg::kChunks];
         row_of(k_raw, w);
 #pragma unroll
         for (int i = 0; i < Cfg::kChunks; ++i) {
-            const uint32_t v[8] = {w[i].x & kNibs, w[i].x >> 4 & kNibs, w[i].y & kNibs, w[i].y >> 4 & kNibs,
-                                   w[i].z & kNibs, w[i].z >> 4 & kNibs, w[i].w & kNibs, w[i].w >> 4 & kNibs};
-            st_cols<8>(tlane + i * 8, v);
+            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            uint32_t v[16];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t x8 = x[j] >> 8;
+                v[4 * j] = nib_lo(x[j]);
+                v[4 * j + 1] = nib_hi(x[j]);
+                v[4 * j + 2] = nib_lo(x8);
+                v[4 * j + 3] = nib_hi(x8);
+            }
+            st_cols<16>(tlane + i * 16, v);
         }
     };
     auto write_v = [&]() {
@@ -331,12 +341,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
             }
         }
     };
-    const uint64_t desc_q = tc::sdesc_sw128(sQ), desc_v = v_desc<D>(sV), desc_p = p_desc<R>(sP);
+    const uint64_t desc_q = q_desc<R>(sQ), desc_v = v_desc<D>(sV), desc_p = p_desc<R>(sP);
     const uint32_t lead = elect();
     auto issue_scores = [&]() {   // (warp 0)
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k)
-            mma_e4m3(lead, tcol + Cfg::kColS, tcol + k * 8, desc_q + (uint64_t)(k * 2), idesc(Cfg::kNS, false), k > 0);
+        for (int k = 0; k < D / 16; ++k)   // (32 bytes of Q's rows; 64 values a block)
+            mma_ts(lead, tcol + Cfg::kColS, tcol + k * 8, desc_q + (uint64_t)((k >> 2) * (R * 128 / 16) + (k & 3) * 2), idesc(Cfg::kNP, false), k > 0);
         commit(lead, &sh.s_full);
     };
     // The first copies of an item (K and scales of its first unit, and V's, in no group
@@ -381,30 +391,18 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
             }
             big = __reduce_max_sync(0xffffffffu, big);
             const int e = norm_exponent(big);
-            // to [2^7, 2^8), 448 being the largest e4m3, and signed so that the largest
-            // product is the largest score (one by one: the factors' product may be infinite)
-            const float f = pow2_biased(254 - e), up = p.scale < 0.f ? -128.f : 128.f;
-            float sum = 0.f;
+            // the largest to [2^8, 2^9), and signed so that the largest product is the largest
+            // score (one by one: the factors' product may be infinite)
+            const float f = pow2_biased(254 - e), up = p.scale < 0.f ? -256.f : 256.f;
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) {
-                // codes 0, 2, 4, 6 of a word are one column of K's row, 1, 3, 5, 7 the next
-                const int d = lane * (D / 32) + j, at = (d & ~7) + (d & 1) * 4 + ((d & 7) >> 1);
-                const float y = x[j] * f * up;
-                const uint32_t q1 = e4m3_of(y), q2 = e4m3_of(y - of_e4m3(q1));
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int n = k * R + r;
-                    sQ[(n >> 3) * 1024 + (n & 7) * 128 + (((at >> 4) ^ (n & 7)) << 4) + (at & 15)] = (uint8_t)(k ? q2 : q1);
-                }
-                sum += of_e4m3(q1) + of_e4m3(q2);
+                // values 0, 4, 1, 5, 2, 6, 3, 7 of eight side by side, as K's
+                const int d = lane * (D / 32) + j, at = (d & 56) + (d & 3) * 2 + (d >> 2 & 1);   // of a block of 64
+                *reinterpret_cast<__half *>(sQ + (d >> 6) * (R * 128) + r * 128 + (((at >> 3) ^ (r & 7)) << 4) + (at & 7) * 2) = __float2half_rn(x[j] * f * up);
             }
-#pragma unroll
-            for (int j = 16; j > 0; j >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, j);
             if (lane == 0) {
-                // 2^9 of the codes less the 2^7 of the queries
-                const float cc = fmaxf(fabsf(p.scale) * kLog2e * pow2_biased(e) * 4.f, 1e-37f);
+                const float cc = fabsf(p.scale) * kLog2e * pow2_biased(e) * (1.f / 256.f);
                 sh.c[r] = big < 0x7F80u ? cc : __uint_as_float(0x7fc00000u);   // a query that is not finite: NaN
-                sh.base[r] = sum * (-8.f / 512.f);
                 sh.lim[r] = r < rows ? it.s.len - it.s.nq + qi + 1 : 0;
             }
         }
@@ -454,23 +452,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
             tc::fence_after();
             float s[R];
             {
-                float s2[2 * R];
-                ld_cols<2 * R>(tlane + Cfg::kColS, s2);
+                ld_cols<R>(tlane + Cfg::kColS, s);
 #pragma unroll
                 for (int r = 0; r < R; r += 4) {
-                    const float4 base = *reinterpret_cast<const float4 *>(sh.base + r), cs = *reinterpret_cast<const float4 *>(sh.c + r),
-                                 m = *reinterpret_cast<const float4 *>(sh.m + r);
-                    float *x = s2 + r, *y = s2 + R + r;
-                    add2(x[0], x[1], y[0], y[1]);
-                    add2(x[2], x[3], y[2], y[3]);
-                    add2(x[0], x[1], base.x, base.y);
-                    add2(x[2], x[3], base.z, base.w);
+                    const float4 cs = *reinterpret_cast<const float4 *>(sh.c + r), m = *reinterpret_cast<const float4 *>(sh.m + r);
+                    float *x = s + r;
                     mul2(x[0], x[1], fk, fk);
                     mul2(x[2], x[3], fk, fk);
                     fma2(x[0], x[1], cs.x, cs.y, -m.x, -m.y);
                     fma2(x[2], x[3], cs.z, cs.w, -m.z, -m.w);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) s[r + j] = x[j];
                 }
             }
             // ---- the next unit's K, whose product runs beside what follows
