@@ -142,7 +142,7 @@ def test_queries_that_are_not_finite_and_see_nothing(nq):
 
 # ---- queries with one value far above the rest -------------------------------------------------------------------
 
-@pytest.mark.parametrize("nq,max_q", [(1, 1), (1, 4096), (5, 1), (5, 5), (70, 1)])
+@pytest.mark.parametrize("nq,max_q", [(1, 1), (1, 4096), (5, 1), (5, 5), (70, 1), (70, 70)])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("above", [9, 11, 13, 17, 20])
 def test_queries_with_a_value_far_above_the_rest(nq, max_q, D, above):

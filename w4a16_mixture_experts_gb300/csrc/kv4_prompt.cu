@@ -31,9 +31,10 @@
 // Precision. A code times its scale has 11 bits, so it is exact in fp16 but for
 // its range: a stage's K rows are less the exponent of the stage's largest K
 // scale (put back in fp32 in the scores), V rows less that of the largest V
-// scale so far (put back at the end; the sums are rescaled when it grows), and a
-// query row less its own. Rows more than 2^14 below the largest lose bits that
-// are below 2^-24 of it. Probabilities are rounded to fp16.
+// scale so far (put back at the end; the sums are rescaled when it grows). Rows more
+// than 2^14 below the largest lose bits that are below 2^-24 of it. A query row
+// enters less its own exponent, its largest value brought to [2^8, 2^9): values below
+// 2^-25 of that are rounded at 2^-33 of it. Probabilities are rounded to fp16.
 #include "kv4_attention.cuh"
 #include "tcgen05.cuh"
 
@@ -309,11 +310,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) big = max(big, max(w[j] & 0x7FFFu, w[j] >> 16 & 0x7FFFu));
                 }
-                const int e = norm_exponent(big);
-                float f = pow2_biased(254 - e);
+                const int e = max(norm_exponent(big), 9);
+                float f = pow2_biased(262 - e);   // the largest to [2^8, 2^9)
                 if (p.scale < 0.f) f = -f;   // so that the largest product is the largest score
                 if (there) lim = it.s.len - it.s.nq + qi + 1;
-                c_row = fabsf(p.scale) * kLog2e * pow2_biased(e);
+                c_row = fabsf(p.scale) * kLog2e * pow2_biased(e - 8);
                 if (big >= 0x7F80u && lim > 0) l0 = __uint_as_float(0x7fc00000u);   // a query that is not finite: NaN, where it sees a key
                 uint8_t *const tile = sQ + wg * Cfg::kTile;
 #pragma unroll
