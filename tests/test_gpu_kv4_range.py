@@ -70,7 +70,7 @@ def _near(q, cache, table, n, max_q, scale=None, floor=2.0 ** -21, rows=None, co
             z = torch.logsumexp(s, -1, keepdim=True)
             p, ka = (s - z).exp(), k[:seen].abs()
             ds = 2 * U32 * (D + 4) * abs(scale) * (x.abs() @ ka.T) + abs(scale) * 2.0 ** -33 * x.abs().amax(-1, keepdim=True) * ka.sum(-1)
-            ds = torch.expm1(2 * ds)
+            ds = torch.expm1(2 * ds).clamp(max=1e30)   # (a finite bound, so that no probability times it is none)
             want = (p * vs[:seen]) @ codes[:seen]
             absolute = codes[:seen].abs()
             mass = (p * vs[:seen]) @ absolute
@@ -157,3 +157,21 @@ def test_queries_with_a_value_far_above_the_rest(nq, max_q, D, above):
     q = (1.6 * _randn(g, nq, G, D)).bfloat16()
     q[..., 4], q[..., 37] = 2.0 ** above, -1.7 * 2.0 ** above
     _near(q, cache, table, n, max_q)
+
+
+# ---- scales far apart in one sequence ------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("copies", [1, 700])
+@pytest.mark.parametrize("which", ["k"])
+@pytest.mark.parametrize("by", [2.0 ** 18, 2.0 ** 26, 2.0 ** 60])
+@pytest.mark.parametrize("nq,max_q", [(6, 1), (6, 6), (6, 4096), (140, 140), (140, 1)])
+def test_one_key_with_a_huge_scale(which, by, nq, max_q, copies):
+    """The last key's scale is far above the others', and only the last query sees it."""
+    g = _gen(nq)
+    n, S, G, D = 500, 16, 4, 128
+    cache, table, page, at = _one_sequence(g, n, S, D)
+    scales = cache.k_scales if which == "k" else cache.v_scales
+    scales[page[-1], 0, at[-1]] *= by
+    q = (1.6 * _randn(g, nq, G, D)).bfloat16()
+    rows = sorted(set(range(0, nq, 17)) | {nq - 2, nq - 1})
+    _near(q, cache, table, n, max_q, rows=rows, copies=copies)

@@ -30,7 +30,10 @@
 //
 // Precision. A code times its scale has 11 bits, so it is exact in fp16 but for
 // its range: a stage's K rows are less the exponent of the stage's largest K
-// scale (put back in fp32 in the scores), V rows less that of the largest V
+// scale (put back in fp32 in the scores). Where a stage's K scales lie more than
+// 2^16 apart (kKeyRange) its K rows are the codes alone and the softmax multiplies
+// each score by its key's scale: a key that a row does not see, or that has no
+// probability, takes nothing from the others. V rows are less the exponent of the largest V
 // scale so far (put back at the end; the sums are rescaled when it grows). Rows more
 // than 2^14 below the largest lose bits that are below 2^-24 of it. A query row
 // enters less its own exponent, its largest value brought to [2^8, 2^9): values below
@@ -100,6 +103,16 @@ template <int N>
 __device__ inline void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ inline void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// A stage's K scales are multiplied into its rows where the smallest is not more than so
+// many octaves below the largest: the products' 11 bits then lie above fp16's smallest.
+constexpr int kKeyRange = 16;
+
+// The exponent of a scale for a smallest one: none where it is zero.
+__device__ inline int low_exponent(float s) {
+    const int e = (int)(__float_as_uint(s) >> 23 & 0xFFu);
+    return s == 0.f ? 1 << 20 : e == 0 ? -7 : e;   // (bf16 has 7 octaves below its smallest normal)
+}
 
 // Descriptor of an operand at a shared address, 128-byte swizzle, 8 rows an atom
 // of 1024 bytes. K-major: the leading stride is not used (1). A row-major
@@ -207,7 +220,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     __shared__ Item s_first;
-    __shared__ int s_E[4], s_F[4], s_red[2][2][2][4];   // a stage's K exponent, V exponent so far (rings of 4 stages)
+    __shared__ int s_E[4], s_F[4], s_red[2][2][3][4];   // a stage's K exponent (0: its rows are codes), V exponent so far (rings of 4 stages)
+    // K scales of a stage whose rows are codes. A ring of 3: the stage three on is written after the scores of
+    // the next have been formed, and those after this one's have been used.
+    __shared__ alignas(16) float s_fk[3][kKeys];
     __shared__ alignas(16) uint16_t s_scales[8][3][2][32];   // of a warp's stages in turn: K's, V's
     volatile int *const abort_flag = &s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -343,12 +359,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                 ++gs;
                 tc::fence_after();
                 const int E = s_E[g & 3], Fn = s_F[g & 3];
-                const float ct = fmaxf(c_row * pow2_biased(E), 1e-37f);
+                float ct = fmaxf(c_row * pow2_biased(E), 1e-37f);
                 float x[128], mx[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) ld32(tS + i * 32, *reinterpret_cast<float(*)[32]>(x + i * 32));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) wait_ld(*reinterpret_cast<float(*)[32]>(x + i * 32));
+                if (E == 0) {
+                    const float4 *const f = reinterpret_cast<const float4 *>(s_fk[g % 3]);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {   // (the factors first: they meet in range)
+                        const float4 k = f[i];
+                        x[4 * i] *= k.x * c_row;
+                        x[4 * i + 1] *= k.y * c_row;
+                        x[4 * i + 2] *= k.z * c_row;
+                        x[4 * i + 3] *= k.w * c_row;
+                    }
+                    ct = 1.f;
+                }
                 if (st * kKeys + kKeys > least) {
                     const int left = lim - st * kKeys;   // keys of the stage that the row sees
 #pragma unroll
@@ -539,10 +567,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                 const float kf = bad ? 0.f : bf16_bits_to_f32(ks), vf = bad ? 0.f : bf16_bits_to_f32(vs);
                 const uint32_t ek = __reduce_max_sync(0xffffffffu, __float_as_uint(kf) >> 23 & 0xFFu);
                 const uint32_t ev = __reduce_max_sync(0xffffffffu, __float_as_uint(vf) >> 23 & 0xFFu);
-                int(&red)[2][4] = s_red[!keys][g & 1];
+                const int low = __reduce_min_sync(0xffffffffu, low_exponent(kf));
+                int(&red)[3][4] = s_red[!keys][g & 1];
                 if (lane == 0) {
                     red[0][w4] = (int)ek;
                     red[1][w4] = (int)ev;
+                    red[2][w4] = low;
                 }
                 if (!(ok = bar_and(keys ? 2 : 3, 128, ok))) break;   // (for all warps of the role at once)
                 int E = 1;
@@ -553,11 +583,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                 }
                 E = min(E, 253);
                 F = min(F, 253);
+                const bool codes = keys && min(min(red[2][0], red[2][1]), min(red[2][2], red[2][3])) < E - kKeyRange;
+                if (codes) s_fk[g % 3][r] = kf;
                 if (keys && r == 0) {
-                    s_E[g & 3] = E;
+                    s_E[g & 3] = codes ? 0 : E;
                     s_F[g & 3] = F;
                 }
-                const __half2 s2 = !keys ? __float2half2_rn(vf * pow2_biased(254 - F)) : bad ? __float2half2_rn(NAN) : __float2half2_rn(kf * pow2_biased(254 - E));
+                const __half2 s2 = __float2half2_rn(!keys ? vf * pow2_biased(254 - F) : bad ? NAN : codes ? 1.f : kf * pow2_biased(254 - E));
 #pragma unroll
                 for (int i = 0; i < Cfg::kChunks; ++i) {
                     const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
