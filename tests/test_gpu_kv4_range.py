@@ -1,8 +1,16 @@
-"""Attention over the 4-bit cache where values lie far apart: scores far below zero, queries with one value far above
-the rest.
+"""Attention over the 4-bit cache where values lie far apart: scores far below zero, queries, keys and values of very
+different sizes in one sequence, long tails of small probabilities.
 
-Tolerances are those that test_gpu_kv4.py derives, key by key: a score's error goes with its own key's products. A query
-value keeps 2^-33 of the row's largest at least (half a step of fp16's smallest, against a largest of 2^8).
+Tolerances are those that test_gpu_kv4.py derives, key by key, with tighter terms where the kernels promise more. With
+p_j the probabilities, v_j = s_j n_j a row of V (scale, codes), C = max_j p_j s_j the weight of the row's largest key:
+ - a score's error goes with its own key's products, so a probability's does: a huge key that has no probability adds
+   nothing to the others' bound;
+ - a query value keeps 2^-33 of the row's largest at least (half a step of fp16's smallest, against a largest of 2^8);
+ - p_j s_j enters the tensor core as fp16 against the row's own largest: off by `floor` * C at most where it is small.
+   2^-31: half of fp16's smallest step, against 2^6 at least; a kernel that scales V by a common power of two takes off
+   p_j alone, at 2^-32 of the largest p, and may do so where the scales seen so far lie within 2^11 of each other,
+   which is 2^-21 of C.
+ - a CTA adds at most its share of the keys, 16 at a time, and the shares' sums are joined.
 """
 import math
 
@@ -162,9 +170,9 @@ def test_queries_with_a_value_far_above_the_rest(nq, max_q, D, above):
 # ---- scales far apart in one sequence ------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("copies", [1, 700])
-@pytest.mark.parametrize("which", ["k"])
 @pytest.mark.parametrize("by", [2.0 ** 18, 2.0 ** 26, 2.0 ** 60])
-@pytest.mark.parametrize("nq,max_q", [(6, 1), (6, 6), (6, 4096), (140, 140), (140, 1)])
+@pytest.mark.parametrize("which,nq,max_q", [("k", 6, 1), ("k", 6, 6), ("k", 6, 4096), ("k", 140, 140), ("k", 140, 1),
+                                              ("v", 6, 1), ("v", 6, 6), ("v", 140, 1)])
 def test_one_key_with_a_huge_scale(which, by, nq, max_q, copies):
     """The last key's scale is far above the others', and only the last query sees it."""
     g = _gen(nq)
@@ -175,3 +183,68 @@ def test_one_key_with_a_huge_scale(which, by, nq, max_q, copies):
     q = (1.6 * _randn(g, nq, G, D)).bfloat16()
     rows = sorted(set(range(0, nq, 17)) | {nq - 2, nq - 1})
     _near(q, cache, table, n, max_q, rows=rows, copies=copies)
+
+
+@pytest.mark.parametrize("copies", [1, 700])
+@pytest.mark.parametrize("first", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("nq,max_q", [(1, 1), (6, 1), (6, 6), (140, 1)])
+def test_scales_spread_over_thirty_octaves(nq, max_q, D, first, copies):
+    """K's and V's scales from 2^-30 to 1, the largest on keys that most rows do not see, or on the first."""
+    g = _gen(nq + D)
+    n, S, G = 1100, 16, 5
+    cache, table, page, at = _one_sequence(g, n, S, D)
+    for scales in (cache.k_scales, cache.v_scales):
+        e = -30 * torch.rand(n, generator=g, device="cuda")
+        if first:
+            e[:3] = 0
+        else:
+            e -= 12                                      # and then far above
+            e[-2:] = 0
+        scales[page, 0, at] = torch.exp2(e).bfloat16()
+    q = (40 * _randn(g, nq, G, D)).bfloat16()
+    rows = sorted(set(range(0, nq, 17)) | {max(nq - 3, 0), nq - 1})
+    _near(q, cache, table, n, max_q, rows=rows, copies=copies)
+
+
+@pytest.mark.parametrize("copies", [1, 700])
+@pytest.mark.parametrize("order", ["up", "down"])
+@pytest.mark.parametrize("nq,max_q", [(1, 1), (6, 6), (140, 1)])
+def test_scales_that_change_along_the_sequence(nq, max_q, order, copies):
+    """V's scales fall or rise by 2^40 from the first key to the last, while the scores favour the small ones."""
+    g = _gen(nq)
+    n, S, G, D = 2000, 32, 2, 64
+    cache, table, page, at = _one_sequence(g, n, S, D)
+    e = -40 * torch.arange(n, device="cuda") / n
+    e = e if order == "down" else e.flip(0)
+    cache.v_scales[page, 0, at] = torch.exp2(e).bfloat16()
+    codes = (_randn(g, n, D) * 1.2).round().clamp(-8, 7)
+    # the score makes up for the scale: exp(score) * scale is about 1 everywhere
+    codes[:, 0] = (-e / 40 * 15 - 8).round().clamp(-8, 7)
+    cache.k_codes[page, 0, at] = _words(codes)
+    cache.k_scales.fill_(0.5)
+    q = (0.3 * _randn(g, nq, G, D)).bfloat16()
+    q[..., 0] = 40 * math.log(2) / 15 / 0.5 * D ** 0.5
+    rows = sorted(set(range(0, nq, 17)) | {nq - 1})
+    _near(q, cache, table, n, max_q, rows=rows, copies=copies)
+
+
+# ---- long tails ---------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("nq,max_q,copies", [(1, 1, 1), (1, 1, 1300), (4, 4, 1300), (10, 10, 1000), (40, 1, 1), (40, 1, 310)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_peak_and_a_long_flat_tail(nq, max_q, copies, D):
+    """One key 18 nats above 2^17 others: the others' mass is small, and all of V that the row has."""
+    g = _gen(D)
+    n, S, G = (1 << 17) + 77, 64, 2
+    cache, table, page, at = _one_sequence(g, n, S, D)
+    codes = torch.zeros(n, D, device="cuda")
+    codes[333] = 7
+    cache.k_codes[page, 0, at] = _words(codes)
+    cache.k_scales.fill_(0.5)
+    values = 5 + (torch.rand(n, D, generator=g, device="cuda") * 2).floor()
+    values[333] = 0
+    cache.v_codes[page, 0, at] = _words(values)
+    cache.v_scales.fill_(0.5)
+    q = torch.full((nq, G, D), 18 / 3.5 / D ** 0.5, device="cuda").bfloat16()
+    _near(q, cache, table, n, max_q, floor=2.0 ** -31, rows=[0, nq - 1], copies=copies)

@@ -58,8 +58,8 @@ struct Attn {
     int Hq, G;
 };
 
-// A part of an item: the running maximum and sum of each row, the exponent of
-// its values, and the rows' values.
+// A part of an item: the exponent taken off each row's scores and the sum of its
+// probabilities, the exponent taken off all its values, and the rows' values.
 __host__ __device__ constexpr int part_floats(int R, int D) { return 2 * R + 4 + R * D; }
 
 // A load that stays where it is written (the compiler would move it down to its
@@ -73,6 +73,12 @@ __device__ inline int ld_here(const int32_t *p) {
 __device__ inline float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ inline float log2_approx(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 

@@ -25,9 +25,17 @@
 // which are rounded at 2^-33 of it. (With K as e4m3 codes q + 8, which take a third
 // of the instructions, and a query as two e4m3 numbers, what a value far above the
 // rest left of them was rounded at 2^-18 of it, and 8 times it passed through the
-// sums of keys that hold zeros beside it.) A V scale multiplies its key's probabilities just
-// before they are rounded to fp16, less the exponent F of the largest V scale so
-// far (a power of two, put back at the end).
+// sums of keys that hold zeros beside it.)
+// A V scale multiplies its key's probabilities just before they are rounded to
+// fp16, so what is rounded is what the key adds to the row. A row's exponents are
+// therefore taken off not against its largest score but against its largest
+// product of probability and scale, which is kept between 2^6 and 2^15: a product
+// is rounded at 2^-31 of the row's largest at most, whatever the scales of keys
+// that the row does not see or that have no probability in it, and a long tail
+// of small ones is not lost. (Against the largest score, with the largest V scale
+// brought to 1, it was 2^-25 of probability 1 and of that scale.) The sum of the
+// probabilities alone follows the same exponent in fp32, up to 2^96 for keys whose
+// values are next to nothing.
 #include <type_traits>
 
 #include "kv4_attention.cuh"
@@ -69,7 +77,7 @@ struct DecodeShared {
     uint64_t s_full, o_full;                    // scores formed, values added
     long long sums[4];
     Item first;
-    int lim[R], we[4];
+    int lim[R], we[4];                          // we: exponents of the warps' largest V scales in the item's first unit
     uint32_t tmem;
 };
 
@@ -415,12 +423,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
         float l[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) l[r] = 0.f;
-        int F = 1;            // biased exponent taken off the V scales
-        float v_top = 0.f;    // 2^(F - 126): they stay below it (0: the first unit takes the branch that sets both)
         int st = st0, slot = 0;   // slot: of this unit's scales
         bool fail = false;        // a wait gave up
         copies_wait<0>();   // (K; V belongs to the next group)
         __syncwarp();
+        {
+            const float fv = at0 != kNone && st * kKeys + tid < it.s.len ? fabsf(bf16_bits_to_f32(sh.scales[warp][0][1][lane])) : 0.f;
+            const uint32_t e = fv > 0.f && fv < INFINITY ? max(__float_as_uint(fv) >> 23, 1u) : 0u, top = __reduce_max_sync(0xffffffffu, e);
+            if (lane == 0) sh.we[warp] = (int)top;
+        }
         write_k();
         __syncwarp();
         at1 = place(st + 1, page1);
@@ -435,6 +446,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
         __syncthreads();
         tc::fence_after();
         if (warp == 0) issue_scores();
+        // the biased exponent taken off all V scales, of the largest of the first unit (a middle for
+        // their range, nothing more)
+        const int we = max(max(sh.we[0], sh.we[1]), max(sh.we[2], sh.we[3])), F = we == 0 ? 127 : min(we, 253);
         for (uint32_t turn = 0; st < st1; ++st, ++turn) {
             const bool more = st + 1 < st1;
             // ---- the key's scores, less the maxima in use. Scales: a row that was not finite
@@ -491,12 +505,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
                 for (int r = 0; r < R; ++r)
                     if (key >= sh.lim[r]) s[r] = -INFINITY;
             }
-            bool over = !(fabsf(fv) < v_top);
+            // ---- probabilities; where one times its V scale would pass 2^15, or itself 2^96, the warp
+            // leaves them until the rows' exponents have followed (and in the first unit, which sets them)
+            const float f = fminf(fmaxf(fv * pow2_biased(254 - F), -0x1p120f), 0x1p120f), log_f = log2_approx(fabsf(f));
+            float top = s[0];
 #pragma unroll
-            for (int r = 0; r < R; ++r) over |= s[r] > 8.f;
-            // ---- probabilities; where a score passed the maximum in use by 2^8, or a V scale its
-            // exponent, the warp leaves them until all have followed
-            over = __any_sync(0xffffffffu, over);
+            for (int r = 1; r < R; ++r) top = fmaxf(top, s[r]);
+            const bool over = __any_sync(0xffffffffu, turn == 0 || top > fminf(15.f - log_f, 96.f));
             const uint32_t p_at = Cfg::kPs == 2 ? (turn & 1) * Cfg::kP : 0;
             auto values_added = [&]() {   // the last unit's values are in the sums, and V and P free
                 if (turn > 0) {
@@ -505,7 +520,6 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
                 }
             };
             auto write_p = [&](bool sum) {
-                const float f = fv * pow2_biased(254 - F);
 #pragma unroll
                 for (int r = 0; r < R; r += 8) {
                     uint32_t h[4];
@@ -535,24 +549,24 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
             if (bar_or(over || fail)) {
                 tc::fence_after();
                 if (bar_or(fail)) break;   // a wait gave up: for all warps at once
-                // ---- all follow: the maxima, the exponent, the sums
-                reduce_rows<R, true>(s, sh.wm[warp]);
-                const uint32_t e = __reduce_max_sync(0xffffffffu, __float_as_uint(fv) >> 23 & 0xFFu);
-                if (lane == 0) sh.we[warp] = (int)e;
+                // ---- all follow: the rows' exponents, then the sums
+                {
+                    float t[R];
+                    const float by = fmaxf(log_f - 6.f, -90.f);
+#pragma unroll
+                    for (int r = 0; r < R; ++r) t[r] = s[r] + by;
+                    reduce_rows<R, true>(t, sh.wm[warp]);
+                }
                 __syncthreads();
-                const int Fn = max(F, min(max(max(sh.we[0], sh.we[1]), max(sh.we[2], sh.we[3])), 253));
-                const float fo = Fn - F > 126 ? 0.f : pow2_biased(127 + F - Fn);
-                F = Fn;
-                v_top = F == 253 ? INFINITY : pow2_biased(F + 1);
-                float up[R];   // how far each row's maximum rises, then 2 to less that
+                float up[R];   // how far each row's exponent rises, then 2 to less that
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     const float x = fmaxf(fmaxf(sh.wm[0][r], sh.wm[1][r]), fmaxf(sh.wm[2][r], sh.wm[3][r]));
                     // (a row that sees no key of the first unit sees none of the later ones)
                     up[r] = turn > 0 ? fmaxf(x, 0.f) : x == kNoMax ? 0.f : x;
-                    if (tid == r) sh.m[r] += up[r];   // (all have read the old maxima before the barriers)
+                    if (tid == r) sh.m[r] += up[r];   // (all have read the old ones before the barriers)
                     s[r] -= up[r];
-                    // (turn 0: nothing to rescale, and a maximum far below zero has no power of two)
+                    // (turn 0: nothing to rescale, and one far below zero has no power of two)
                     up[r] = turn > 0 ? exp2_approx(-up[r]) : 1.f;
                     l[r] *= up[r];
                 }
@@ -561,7 +575,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
                     ld_cols<R>(tlane + Cfg::kColO, o);
                     uint32_t w[R];
 #pragma unroll
-                    for (int r = 0; r < R; ++r) w[r] = __float_as_uint(o[r] * (up[r] * fo));
+                    for (int r = 0; r < R; ++r) w[r] = __float_as_uint(o[r] * up[r]);
                     st_cols<R>(tlane + Cfg::kColO, w);
                     tc::wait_st();
                 }
