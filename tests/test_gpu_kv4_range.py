@@ -248,3 +248,20 @@ def test_a_peak_and_a_long_flat_tail(nq, max_q, copies, D):
     cache.v_scales.fill_(0.5)
     q = torch.full((nq, G, D), 18 / 3.5 / D ** 0.5, device="cuda").bfloat16()
     _near(q, cache, table, n, max_q, floor=2.0 ** -31, rows=[0, nq - 1], copies=copies)
+
+
+# ---- zeros ----------------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("then", [1.0, 2.0 ** -60, 2.0 ** 60])
+@pytest.mark.parametrize("nq,max_q", [(1, 1), (6, 6), (140, 1)])
+def test_zero_scales_before_others(nq, max_q, then):
+    """The first keys' rows are zeros, so that their scales give no exponent, then come others, some of them far apart."""
+    g = _gen(nq)
+    n, S, G, D = 1000, 16, 4, 64
+    cache, table, page, at = _one_sequence(g, n, S, D)
+    cache.k_scales[page[:300], 0, at[:300]] = 0
+    cache.v_scales[page[:300], 0, at[:300]] = 0
+    cache.v_scales[page[300:], 0, at[300:]] *= then
+    cache.v_scales[page[700:], 0, at[700:]] *= 2.0 ** -20
+    q = (1.6 * _randn(g, nq, G, D)).bfloat16()
+    _near(q, cache, table, n, max_q, rows=sorted({0, nq // 2, nq - 1}), copies=700)

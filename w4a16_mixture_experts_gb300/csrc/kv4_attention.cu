@@ -51,11 +51,12 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Attn p, int R) {
             Mn = fmaxf(Mn, __shfl_xor_sync(0xffffffffu, Mn, o));
             Fn = max(Fn, __shfl_xor_sync(0xffffffffu, Fn, o));
         }
-        const float w = exp2_approx(m - Mn), down = exp2_approx(M - Mn);
-        float sum = l * w;
+        // (halves: a sum of probabilities may be far above 1, its weight below fp32's range)
+        const float w2 = exp2_approx(0.5f * (m - Mn)), down2 = exp2_approx(0.5f * (M - Mn)), w = w2 * w2, down = down2 * down2;
+        float sum = l * w2 * w2;
 #pragma unroll
         for (int o = G / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        L = L * down + sum;
+        L = L * down2 * down2 + sum;
         const float wv = Fn - f > 126 ? 0.f : w * pow2_biased(127 + f - Fn), dv = Fn - F > 126 ? 0.f : down * pow2_biased(127 + F - Fn);
         acc = make_float4(acc.x * dv, acc.y * dv, acc.z * dv, acc.w * dv);
         M = Mn;

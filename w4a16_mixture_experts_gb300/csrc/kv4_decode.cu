@@ -558,7 +558,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
                     reduce_rows<R, true>(t, sh.wm[warp]);
                 }
                 __syncthreads();
-                float up[R];   // how far each row's exponent rises, then 2 to less that
+                float up[R];   // how far each row's exponent rises, then 2 to half of less that (all of it may be
+                               // below fp32's range where the sum of probabilities is far above it)
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     const float x = fmaxf(fmaxf(sh.wm[0][r], sh.wm[1][r]), fmaxf(sh.wm[2][r], sh.wm[3][r]));
@@ -567,15 +568,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
                     if (tid == r) sh.m[r] += up[r];   // (all have read the old ones before the barriers)
                     s[r] -= up[r];
                     // (turn 0: nothing to rescale, and one far below zero has no power of two)
-                    up[r] = turn > 0 ? exp2_approx(-up[r]) : 1.f;
-                    l[r] *= up[r];
+                    up[r] = turn > 0 ? exp2_approx(-0.5f * up[r]) : 1.f;
+                    l[r] = l[r] * up[r] * up[r];
                 }
                 if (turn > 0) {
                     float o[R];
                     ld_cols<R>(tlane + Cfg::kColO, o);
                     uint32_t w[R];
 #pragma unroll
-                    for (int r = 0; r < R; ++r) w[r] = __float_as_uint(o[r] * up[r]);
+                    for (int r = 0; r < R; ++r) w[r] = __float_as_uint(o[r] * up[r] * up[r]);
                     st_cols<R>(tlane + Cfg::kColO, w);
                     tc::wait_st();
                 }
