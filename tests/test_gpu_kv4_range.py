@@ -170,9 +170,9 @@ def test_queries_with_a_value_far_above_the_rest(nq, max_q, D, above):
 # ---- scales far apart in one sequence ------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("copies", [1, 700])
+@pytest.mark.parametrize("which", ["k", "v"])
 @pytest.mark.parametrize("by", [2.0 ** 18, 2.0 ** 26, 2.0 ** 60])
-@pytest.mark.parametrize("which,nq,max_q", [("k", 6, 1), ("k", 6, 6), ("k", 6, 4096), ("k", 140, 140), ("k", 140, 1),
-                                              ("v", 6, 1), ("v", 6, 6), ("v", 140, 1)])
+@pytest.mark.parametrize("nq,max_q", [(6, 1), (6, 6), (6, 4096), (140, 140), (140, 1)])
 def test_one_key_with_a_huge_scale(which, by, nq, max_q, copies):
     """The last key's scale is far above the others', and only the last query sees it."""
     g = _gen(nq)
@@ -188,7 +188,7 @@ def test_one_key_with_a_huge_scale(which, by, nq, max_q, copies):
 @pytest.mark.parametrize("copies", [1, 700])
 @pytest.mark.parametrize("first", [False, True])
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("nq,max_q", [(1, 1), (6, 1), (6, 6), (140, 1)])
+@pytest.mark.parametrize("nq,max_q", [(1, 1), (1, 4096), (6, 1), (6, 6), (140, 140), (140, 1)])
 def test_scales_spread_over_thirty_octaves(nq, max_q, D, first, copies):
     """K's and V's scales from 2^-30 to 1, the largest on keys that most rows do not see, or on the first."""
     g = _gen(nq + D)
@@ -209,7 +209,7 @@ def test_scales_spread_over_thirty_octaves(nq, max_q, D, first, copies):
 
 @pytest.mark.parametrize("copies", [1, 700])
 @pytest.mark.parametrize("order", ["up", "down"])
-@pytest.mark.parametrize("nq,max_q", [(1, 1), (6, 6), (140, 1)])
+@pytest.mark.parametrize("nq,max_q", [(1, 1), (1, 4096), (6, 6), (140, 140)])
 def test_scales_that_change_along_the_sequence(nq, max_q, order, copies):
     """V's scales fall or rise by 2^40 from the first key to the last, while the scores favour the small ones."""
     g = _gen(nq)
@@ -231,7 +231,7 @@ def test_scales_that_change_along_the_sequence(nq, max_q, order, copies):
 
 # ---- long tails ---------------------------------------------------------------------------------------------------
 
-@pytest.mark.parametrize("nq,max_q,copies", [(1, 1, 1), (1, 1, 1300), (4, 4, 1300), (10, 10, 1000), (40, 1, 1), (40, 1, 310)])
+@pytest.mark.parametrize("nq,max_q,copies", [(1, 1, 1), (1, 1, 1300), (4, 4, 1300), (10, 10, 1000), (40, 40, 1), (40, 40, 310)])
 @pytest.mark.parametrize("D", [64, 128])
 def test_a_peak_and_a_long_flat_tail(nq, max_q, copies, D):
     """One key 18 nats above 2^17 others: the others' mass is small, and all of V that the row has."""
@@ -253,7 +253,7 @@ def test_a_peak_and_a_long_flat_tail(nq, max_q, copies, D):
 # ---- zeros ----------------------------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("then", [1.0, 2.0 ** -60, 2.0 ** 60])
-@pytest.mark.parametrize("nq,max_q", [(1, 1), (6, 6), (140, 1)])
+@pytest.mark.parametrize("nq,max_q", [(1, 1), (6, 6), (140, 140)])
 def test_zero_scales_before_others(nq, max_q, then):
     """The first keys' rows are zeros, so that their scales give no exponent, then come others, some of them far apart."""
     g = _gen(nq)

@@ -29,15 +29,18 @@
 // rescaled only when a row's maximum passes the one in use by 2^8.
 //
 // Precision. A code times its scale has 11 bits, so it is exact in fp16 but for
-// its range: a stage's K rows are less the exponent of the stage's largest K
-// scale (put back in fp32 in the scores). Where a stage's K scales lie more than
-// 2^16 apart (kKeyRange) its K rows are the codes alone and the softmax multiplies
-// each score by its key's scale: a key that a row does not see, or that has no
-// probability, takes nothing from the others. V rows are less the exponent of the largest V
-// scale so far (put back at the end; the sums are rescaled when it grows). Rows more
-// than 2^14 below the largest lose bits that are below 2^-24 of it. A query row
-// enters less its own exponent, its largest value brought to [2^8, 2^9): values below
-// 2^-25 of that are rounded at 2^-33 of it. Probabilities are rounded to fp16.
+// its range: K and V rows are less the exponent of the largest K or V scale so far
+// (K's put back in fp32 in the scores, V's at the end; the sums are rescaled when
+// it grows). From the stage on where the K scales so far lie more than 2^16 apart
+// (kKeyRange), or the V scales more than 2^10 (kValueRange), the rows are the codes alone,
+// and the softmax multiplies scores and probabilities by the keys' scales in fp32: a
+// key that a row does not see, or that has no probability in it, takes nothing from
+// the others. A query row enters less its own exponent, its largest value brought
+// to [2^8, 2^9): values below 2^-25 of that are rounded at 2^-33 of it.
+// What is rounded to fp16 for the second product is a probability against the row's
+// largest so far, at 2^7 to 2^15, so at 2^-32 of the largest at most (at 1, a tail of
+// 2^17 keys below 2^-25 was lost); with codes, its product with the V scale against
+// the row's largest such product.
 #include "kv4_attention.cuh"
 #include "tcgen05.cuh"
 
@@ -70,7 +73,7 @@ struct PromptCfg {
     static constexpr int kSmem = (2 + 2 * kStages) * kTile + 2 * kRaw;
     // Shared addresses of the operands, known here so that their descriptors are constants: the
     // kernel's other shared memory lies below (the kernel checks it).
-    static constexpr int kAtQ = 8192, kAtK = kAtQ + 2 * kTile, kAtV = kAtK + kStages * kTile;
+    static constexpr int kAtQ = 10240, kAtK = kAtQ + 2 * kTile, kAtV = kAtK + kStages * kTile;
 };
 
 struct Bars {
@@ -104,15 +107,34 @@ __device__ inline void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u3
 template <int N>
 __device__ inline void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// A stage's K scales are multiplied into its rows where the smallest is not more than so
-// many octaves below the largest: the products' 11 bits then lie above fp16's smallest.
-constexpr int kKeyRange = 16;
+// Octaves between the largest scale and the smallest so far up to which scales are
+// multiplied into the rows. K's: the products' 11 bits lie above fp16's smallest. V's: a probability's rounding is 2^-22 of what the row's largest adds at most.
+constexpr int kKeyRange = 16, kValueRange = 10;
 
-// The exponent of a scale for a smallest one: none where it is zero.
-__device__ inline int low_exponent(float s) {
-    const int e = (int)(__float_as_uint(s) >> 23 & 0xFFu);
-    return s == 0.f ? 1 << 20 : e == 0 ? -7 : e;   // (bf16 has 7 octaves below its smallest normal)
-}
+// The exponents of the scales so far, K's or V's of an item.
+struct Range {
+    int top = 1, low = 1 << 20;
+    __device__ bool holds(float s) const {   // (a zero has none)
+        const int e = (int)(__float_as_uint(s) >> 23 & 0xFFu);
+        return s == 0.f || (e <= top && e >= low);
+    }
+    __device__ void take(float s, int *tops, int *lows, int w4, int lane) const {   // a warp's
+        const int e = (int)(__float_as_uint(s) >> 23 & 0xFFu);
+        const int t = (int)__reduce_max_sync(0xffffffffu, (uint32_t)e);
+        const int l = __reduce_min_sync(0xffffffffu, s == 0.f ? 1 << 20 : e == 0 ? -7 : e);   // (bf16 has 7 octaves below its smallest normal)
+        if (lane == 0) {
+            tops[w4] = t;
+            lows[w4] = l;
+        }
+    }
+    __device__ void join(const int *tops, const int *lows) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            top = max(top, tops[i]);
+            low = min(low, lows[i]);
+        }
+    }
+};
 
 // Descriptor of an operand at a shared address, 128-byte swizzle, 8 rows an atom
 // of 1024 bytes. K-major: the leading stride is not used (1). A row-major
@@ -187,6 +209,78 @@ __device__ inline void add2(float &a, float &b, float c, float d) {
         : "f"(c), "f"(d));
 }
 
+// The softmax of a stage whose rows are codes: K's scales, V's less its exponent, and
+// what the latter adds to a score to give the exponent of the product, less 7.
+struct Scales {
+    float k[kKeys], v[kKeys], by[kKeys];
+};
+struct CodesStage {
+    const Scales &scales;
+    float c_row;
+    int left, up;        // keys of the stage that the row sees; how far V's exponent has risen
+    bool sums, codes;    // there are sums so far; they are of stages of codes
+};
+
+// A thread's row (m, l0, l1), 32 keys at a time. Such stages come last in an item and have
+// a loop of their own: as a branch in the other one they cost all prompts 4-7%, in line or not.
+template <int D>
+__device__ inline void codes_stage(float (&row)[3], uint32_t tS, uint32_t tO, const CodesStage &a) {
+    float m = row[0], l0 = row[1], l1 = row[2];
+    auto scores = [&](int i, float (&x)[32]) {
+        ld32(tS + i * 32, x);
+        wait_ld(x);
+        const int left = a.left - i * 32;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {   // (the factors first: they meet in range)
+            const float4 k = *reinterpret_cast<const float4 *>(&a.scales.k[i * 32 + j]);
+            x[j] = j < left ? x[j] * (k.x * a.c_row) : -INFINITY;
+            x[j + 1] = j + 1 < left ? x[j + 1] * (k.y * a.c_row) : -INFINITY;
+            x[j + 2] = j + 2 < left ? x[j + 2] * (k.z * a.c_row) : -INFINITY;
+            x[j + 3] = j + 3 < left ? x[j + 3] * (k.w * a.c_row) : -INFINITY;
+        }
+    };
+    float big = -INFINITY;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        float x[32];
+        scores(i, x);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) big = fmaxf(big, x[j] + a.scales.by[i * 32 + j]);
+    }
+    if (__any_sync(0xffffffffu, !a.codes || big > m + 8.f || a.up)) {
+        // (from scores to products: what the row has may lie kValueRange below)
+        // (in halves: a sum of probabilities may lie far above 1, the factor below fp32's range)
+        const float mn = fmaxf(a.codes ? m : m - kValueRange, big), down = exp2_approx(0.5f * (m - mn));
+        m = mn;
+        l0 = l0 * down * down;
+        l1 = l1 * down * down;
+        if (a.sums) {
+            const float fo = a.up > 126 ? 0.f : down * down * pow2_biased(127 - a.up);
+#pragma unroll 1
+            for (int i = 0; i < D / 16; ++i) rescale16(tO + i * 16, fo);
+        }
+    }
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {   // (the probabilities lie in columns that have been read)
+        float x[32];
+        uint32_t pr[16];
+        scores(i, x);
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            const float2 f = *reinterpret_cast<const float2 *>(&a.scales.v[i * 32 + j]);
+            const float y = exp2_approx(x[j] - m), z = exp2_approx(x[j + 1] - m);
+            l0 += y;
+            l1 += z;
+            const __half2 v = __floats2half2_rn(y * f.x, z * f.y);
+            pr[j >> 1] = *reinterpret_cast<const uint32_t *>(&v);
+        }
+        st16(tS + i * 16, pr);
+    }
+    row[0] = m;
+    row[1] = l0;
+    row[2] = l1;
+}
+
 // 8 codes of a word, times s, as the chunk of 8 fp16 values in the order
 // 0, 4, 1, 5, 2, 6, 3, 7 (queries lie in the same order; the output's columns
 // are put back at the end).
@@ -220,10 +314,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     __shared__ Item s_first;
-    __shared__ int s_E[4], s_F[4], s_red[2][2][3][4];   // a stage's K exponent (0: its rows are codes), V exponent so far (rings of 4 stages)
-    // K scales of a stage whose rows are codes. A ring of 3: the stage three on is written after the scores of
-    // the next have been formed, and those after this one's have been used.
-    __shared__ alignas(16) float s_fk[3][kKeys];
+    __shared__ alignas(16) int s_E[4], s_F[4], s_red[2][2][4][4];   // the K exponent (0: the rows are codes) and V exponent of a stage (rings of 4)
+    // Scales of a stage of codes. A ring of 3: the stage three on is written after the scores of the next
+    // have been formed, and those after this one's have been used.
+    __shared__ alignas(16) Scales s_scale[3];
     __shared__ alignas(16) uint16_t s_scales[8][3][2][32];   // of a warp's stages in turn: K's, V's
     volatile int *const abort_flag = &s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -351,32 +445,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                 if (lane == 0) mbar_arrive(&bars.q_full);
             }
             const int least = __reduce_min_sync(0xffffffffu, lim);
-            float m = kNoMax;
+            float m = kNoMax;   // the exponent taken off: that of the largest probability (or product), less 7 to 15
             int F = 1;
-            for (int st = st0; st < st1 && ok; ++st, ++g) {
+            int st = st0;
+            for (; st < st1 && ok; ++st, ++g) {
                 if (!mine) continue;
                 if (!(ok = wait(&bars.s_full[wg], gs & 1, abort_flag))) break;
                 ++gs;
                 tc::fence_after();
                 const int E = s_E[g & 3], Fn = s_F[g & 3];
-                float ct = fmaxf(c_row * pow2_biased(E), 1e-37f);
-                float x[128], mx[4];
+                if (E == 0) break;
+                float x[128];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) ld32(tS + i * 32, *reinterpret_cast<float(*)[32]>(x + i * 32));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) wait_ld(*reinterpret_cast<float(*)[32]>(x + i * 32));
-                if (E == 0) {
-                    const float4 *const f = reinterpret_cast<const float4 *>(s_fk[g % 3]);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {   // (the factors first: they meet in range)
-                        const float4 k = f[i];
-                        x[4 * i] *= k.x * c_row;
-                        x[4 * i + 1] *= k.y * c_row;
-                        x[4 * i + 2] *= k.z * c_row;
-                        x[4 * i + 3] *= k.w * c_row;
-                    }
-                    ct = 1.f;
-                }
+                const float ct = fmaxf(c_row * pow2_biased(E), 1e-37f);
+                float mx[4];
                 if (st * kKeys + kKeys > least) {
                     const int left = lim - st * kKeys;   // keys of the stage that the row sees
 #pragma unroll
@@ -388,9 +473,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
 #pragma unroll
                 for (int j = 4; j < 128; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
                 const float big = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * ct;
-                if (__any_sync(0xffffffffu, big > m + 8.f || Fn != F)) {
-                    // a new maximum (or exponent of V): the row's sums so far follow it
-                    const float mn = fmaxf(m, big);
+                if (__any_sync(0xffffffffu, big > m + 15.f || Fn != F)) {
+                    // a new exponent (or V's): the row's sums so far follow it
+                    const float mn = fmaxf(m, big - 7.f);
                     const float down = exp2_approx(m - mn);
                     m = mn;
                     l0 *= down;
@@ -417,6 +502,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                     }
                     st16(tS + (i >> 1), pr);
                 }
+                tc::wait_st();
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.p_full[wg]);
+            }
+            // ---- codes from here on
+            for (bool codes = false; st < st1 && ok; ++st, ++g) {
+                if (codes) {   // (the first one's scores have been waited for)
+                    if (!(ok = wait(&bars.s_full[wg], gs & 1, abort_flag))) break;
+                    ++gs;
+                    tc::fence_after();
+                }
+                const int Fn = s_F[g & 3];
+                float state[3] = {m, l0, l1};
+                codes_stage<D>(state, tS, tO, CodesStage{s_scale[g % 3], c_row, lim - st * kKeys, Fn - F, st > st0, codes});
+                m = state[0];
+                l0 = state[1];
+                l1 = state[2];
+                F = Fn;
+                codes = true;
                 tc::wait_st();
                 tc::fence_before();
                 __syncwarp();
@@ -542,7 +647,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                 copies_commit();
             };
             uint32_t at0 = place(st0, page_of(st0)), at1 = kNone;
-            int page = page_of(st0 + 1), slot = 0, F = 1;
+            int page = page_of(st0 + 1), slot = 0, E = 1, F = 1;
+            Range k_range, v_range;
+            bool codes = false;   // the scales so far lie too far apart
             copy(at0, 0);
             for (int st = st0; st < st1; ++st, ++g) {
                 const int b = g % kStages;
@@ -562,34 +669,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                 }
                 at0 = at1;
                 ok = wait(&empty[b], ((g / kStages) & 1) ^ 1, abort_flag);
-                // ---- the stage's exponents; a row that was not finite: K becomes NaN, V zero
+                // ---- the exponents; a row that was not finite: K becomes NaN, V zero
                 const bool bad = !finite_bits(ks) || !finite_bits(vs);
                 const float kf = bad ? 0.f : bf16_bits_to_f32(ks), vf = bad ? 0.f : bf16_bits_to_f32(vs);
-                const uint32_t ek = __reduce_max_sync(0xffffffffu, __float_as_uint(kf) >> 23 & 0xFFu);
-                const uint32_t ev = __reduce_max_sync(0xffffffffu, __float_as_uint(vf) >> 23 & 0xFFu);
-                const int low = __reduce_min_sync(0xffffffffu, low_exponent(kf));
-                int(&red)[3][4] = s_red[!keys][g & 1];
-                if (lane == 0) {
-                    red[0][w4] = (int)ek;
-                    red[1][w4] = (int)ev;
-                    red[2][w4] = low;
+                // (most stages change nothing: that is seen at the barrier alone. With four reductions a warp
+                // for each stage's own exponents the prompt chunk took 756 us, so 732; with the first stage's
+                // before the wait 850)
+                if (st == st0 || !bar_and(keys ? 2 : 3, 128, ok && k_range.holds(kf) && v_range.holds(vf))) {
+                    int(&red)[4][4] = s_red[!keys][g & 1];   // (a stage has a barrier at least: the last stage's may still be read)
+                    k_range.take(kf, red[0], red[1], w4, lane);
+                    v_range.take(vf, red[2], red[3], w4, lane);
+                    if (!(ok = bar_and(keys ? 2 : 3, 128, ok))) break;   // (for all warps of the role at once)
+                    k_range.join(red[0], red[1]);
+                    v_range.join(red[2], red[3]);
+                    // (with codes V's exponent stays, as a middle for their range)
+                    if (!codes) {
+                        codes = k_range.low < k_range.top - kKeyRange || v_range.low < v_range.top - kValueRange;
+                        if (!codes || F == 1) F = min(v_range.top, 253);
+                        E = codes ? 0 : min(k_range.top, 253);
+                    }
                 }
-                if (!(ok = bar_and(keys ? 2 : 3, 128, ok))) break;   // (for all warps of the role at once)
-                int E = 1;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    E = max(E, red[0][i]);
-                    F = max(F, red[1][i]);
+                if (keys) {
+                    if (codes) {
+                        const float f = fminf(fmaxf(vf * pow2_biased(254 - F), -0x1p120f), 0x1p120f);
+                        Scales &to = s_scale[g % 3];
+                        to.k[r] = kf;
+                        to.v[r] = f;
+                        to.by[r] = fmaxf(log2_approx(fabsf(f)) - 7.f, -90.f);
+                    }
+                    if (r == 0) {
+                        s_E[g & 3] = E;
+                        s_F[g & 3] = F;
+                    }
                 }
-                E = min(E, 253);
-                F = min(F, 253);
-                const bool codes = keys && min(min(red[2][0], red[2][1]), min(red[2][2], red[2][3])) < E - kKeyRange;
-                if (codes) s_fk[g % 3][r] = kf;
-                if (keys && r == 0) {
-                    s_E[g & 3] = codes ? 0 : E;
-                    s_F[g & 3] = F;
-                }
-                const __half2 s2 = __float2half2_rn(!keys ? vf * pow2_biased(254 - F) : bad ? NAN : codes ? 1.f : kf * pow2_biased(254 - E));
+                const float factor = keys && bad ? NAN : codes ? 1.f : keys ? kf * pow2_biased(254 - E) : vf * pow2_biased(254 - F);
+                const __half2 s2 = __float2half2_rn(factor);
 #pragma unroll
                 for (int i = 0; i < Cfg::kChunks; ++i) {
                     const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
