@@ -22,7 +22,7 @@ struct SmemAttr {
     int bytes;
     bool done[kMaxDevices];
 };
-constexpr int kMaxSmemKernels = 16;   // kernels that raise their shared-memory limit (9 today)
+constexpr int kMaxSmemKernels = 32;   // kernels that raise their shared-memory limit (20 today)
 SmemAttr g_attrs[kMaxSmemKernels];
 int g_nattrs = 0;
 std::mutex g_attrs_mu;   // callers may launch from several host threads
