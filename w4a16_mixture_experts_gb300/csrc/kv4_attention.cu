@@ -105,6 +105,7 @@ cudaError_t launch_join(const Attn &p, int R, int grid, cudaStream_t s) {
 }  // namespace
 
 size_t kv4_workspace_bytes(int T, int Hq, int Hkv, int D) {
+    if (T == 0) return sizeof(Ctrl);   // (nothing is launched)
     const bool few = (long long)T * (Hq / Hkv) <= kDecodeRows;
     const size_t stream = 2 * kMaxCtas * sizeof(float) * (size_t)part_floats(kDecodeRows, D);
     const size_t prompt = 2 * kMaxPromptCtas * sizeof(float) * (size_t)part_floats(kPromptRows, D);
