@@ -1,5 +1,6 @@
 """The attention block's calls where there is nothing to do, and what the binding checks before them: on the CPU."""
 import pytest
+import torch
 
 import w4a16_mixture_experts_gb300 as moe
 from w4a16_mixture_experts_gb300 import _build
@@ -21,3 +22,43 @@ def test_a_batch_of_no_tokens_needs_what_its_size_says(L, Hq, Hkv, D):
         assert _attend(L, c=c, Hq=Hq, T=0, B=b, cu=cu, q=None, out=None, n=n - 1) == WORKSPACE
     # what the binding makes for such a batch
     assert moe.kv4_workspace(0, Hq, Hkv, D, device="cpu").numel() == n == 256
+
+
+class _OnGpu(torch.Tensor):
+    """A tensor that says it is on the GPU: for checks that come before anything is launched."""
+    is_cuda = property(lambda self: True)
+
+
+def _fake_cache(n=4, h=2, p=16, w=16):
+    on = lambda *s, dtype: torch.zeros(*s, dtype=dtype).as_subclass(_OnGpu)  # noqa: E731
+    return moe.Kv4Cache(on(n, h, p, w, dtype=torch.int32), on(n, h, p, dtype=torch.bfloat16),
+                        on(n, h, p, w, dtype=torch.int32), on(n, h, p, dtype=torch.bfloat16))
+
+
+def test_a_cache_is_checked_at_every_call():
+    """A tensor at the same address with another shape, stride or type is another tensor."""
+    cache = _fake_cache()
+    c, h, d = cache.c()
+    assert (c.n_pages, c.Hkv, c.page_size, c.D, h, d) == (4, 2, 16, 128, 2, 128) and c.v_codes == cache.v_codes.data_ptr()
+    for name, others in (("k_scales", (lambda t: t[:2], lambda t: t.transpose(0, 1), lambda t: t.view(torch.int16), lambda t: t.view(-1))),
+                         ("v_scales", (lambda t: t[:3], lambda t: t[..., ::2], lambda t: t.view(torch.float16))),
+                         ("v_codes", (lambda t: t[:1], lambda t: t.view(4, 2, 32, 8), lambda t: t.view(torch.float32), lambda t: t[..., :8])),
+                         ("k_codes", (lambda t: t[:3], lambda t: t.view(torch.float32), lambda t: t.transpose(1, 2), lambda t: t.view(4, -1)))):
+        kept = getattr(cache, name)
+        for other in others:
+            view = other(kept)
+            assert view.data_ptr() == kept.data_ptr()
+            setattr(cache, name, view)
+            with pytest.raises(ValueError):
+                cache.c()
+        setattr(cache, name, kept)
+        cache.c()
+    cache.v_scales = None
+    with pytest.raises(TypeError):
+        cache.c()
+    # resized in place: the address stays
+    cache = _fake_cache()
+    cache.c()
+    cache.k_scales.resize_(1, 2, 16)
+    with pytest.raises(ValueError):
+        cache.c()

@@ -406,34 +406,42 @@ def moe_w8a16_workspace_size(T: int, N: int, K: int, gs: int) -> int:
     return n.value
 
 
+_BF16, _I32, _F32, _Tensor = torch.bfloat16, torch.int32, torch.float32, torch.Tensor
+
+
 class Kv4Cache:
     """One layer's paged 4-bit KV cache: codes int32 [pages, Hkv, page_size, D/8] (q + 8, eight to a
     word, lowest nibble first) and scales bf16 [pages, Hkv, page_size], of K and of V. The slot of a
     token is page * page_size + its place in the page. Iterates over its four tensors."""
-    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "_c")
+    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales")
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales):
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
-        self._c = None
 
     def __iter__(self):
         return iter((self.k_codes, self.k_scales, self.v_codes, self.v_scales))
 
-    def c(self) -> moe_kv4_cache:
-        """The C struct, formed (and the tensors checked) anew where a tensor's memory has moved."""
+    def c(self):
+        """(C struct, KV heads, D). The tensors are checked at every call, also where one has been
+        replaced, resized or viewed anew at the same address."""
         kc, ks, vc, vs = self.k_codes, self.k_scales, self.v_codes, self.v_scales
-        at = (kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), kc.shape)
-        if self._c is None or self._c[0] != at:
+        try:
+            n, h, p, w = shape = kc.shape
+            rows = shape[:3]
+            good = (kc.dtype is _I32 and vc.dtype is _I32 and ks.dtype is _BF16 and vs.dtype is _BF16
+                    and vc.shape == shape and ks.shape == rows and vs.shape == rows
+                    and kc.is_cuda and ks.is_cuda and vc.is_cuda and vs.is_cuda
+                    and kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and vs.is_contiguous())
+        except (AttributeError, ValueError):   # not tensors, or of other dimensions
+            good = False
+        if not good:
             _need(kc, "k_codes", torch.int32, 4)
             _need(ks, "k_scales", torch.bfloat16, 3)
             _need(vc, "v_codes", torch.int32, 4)
             _need(vs, "v_scales", torch.bfloat16, 3)
-            n, h, p, w = kc.shape
-            if vc.shape != kc.shape or ks.shape != (n, h, p) or vs.shape != (n, h, p):
-                raise ValueError("a cache holds codes [pages, Hkv, page_size, D/8] and scales [pages, Hkv, page_size], "
-                                 "got %s %s %s %s" % tuple(tuple(t.shape) for t in self))
-            self._c = at, moe_kv4_cache(*at[:4], n, h, p, w * 8), h, w * 8
-        return self._c
+            raise ValueError("a cache holds codes [pages, Hkv, page_size, D/8] and scales [pages, Hkv, page_size], "
+                             "got %s %s %s %s" % tuple(tuple(t.shape) for t in self))
+        return moe_kv4_cache(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), n, h, p, w * 8), h, w * 8
 
 
 def kv4_cache(n_pages: int, Hkv: int, page_size: int, D: int, device=None) -> Kv4Cache:
@@ -458,7 +466,6 @@ def kv4_workspace(T: int = 0, Hq: int = 1, Hkv: int = 1, D: int = 128, device=No
     return torch.zeros(n, dtype=torch.uint8, device=device if device is not None else "cuda")
 
 
-_BF16, _I32, _F32, _Tensor = torch.bfloat16, torch.int32, torch.float32, torch.Tensor
 _strides = {}   # (token, head) -> the struct: few pairs occur, and forming one costs more than finding it
 
 
@@ -500,7 +507,7 @@ def _vec(t, name, dtype, n=None):
 
 def _cache(c):
     """(C struct, KV heads, D) of a Kv4Cache, or of four tensors in its order."""
-    return (c if isinstance(c, Kv4Cache) else Kv4Cache(*c)).c()[1:]
+    return (c if isinstance(c, Kv4Cache) else Kv4Cache(*c)).c()
 
 
 def moe_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6,
