@@ -62,3 +62,42 @@ def test_a_cache_is_checked_at_every_call():
     cache.k_scales.resize_(1, 2, 16)
     with pytest.raises(ValueError):
         cache.c()
+
+
+class _Calls:
+    """Stands for the library: notes a call's arguments and answers OK."""
+
+    def __init__(self):
+        self.args = {}
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.args[name] = args
+            return OK
+        return call
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    c = _Calls()
+    monkeypatch.setattr(moe, "lib", lambda: c)
+    monkeypatch.setattr(moe, "_stream", lambda s: 0)
+    return c.args
+
+
+def _on(*shape, dtype):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(_OnGpu)
+
+
+@pytest.mark.parametrize("T,B,cu,given,chosen", [(6, 6, False, None, 1), (6, 6, False, 3, 3), (500, 1, True, None, 500),
+                                                 (24, 6, True, None, 4), (25, 6, True, None, 5), (6, 6, True, None, 1),
+                                                 (500, 1, True, 1, 1), (0, 0, True, None, 0), (0, 2, True, None, 0)])
+def test_max_q_left_out(calls, T, B, cu, given, chosen):
+    """A prompt whose caller leaves max_q out does not go to the kernel for single tokens."""
+    q = _on(T, 4, 128, dtype=torch.bfloat16)
+    kw = {} if given is None else dict(max_q=given)
+    moe.moe_kv4_attention(q, _fake_cache(), _on(B, 3, dtype=torch.int32), _on(B, dtype=torch.int32),
+                          cu_q=_on(B + 1, dtype=torch.int32) if cu else None, out=_on(T, 4, 128, dtype=torch.bfloat16),
+                          ws=_on(1 << 10, dtype=torch.uint8), **kw)
+    args = calls["moe_kv4_attention"]
+    assert args[7:11] == (B, T, 4, chosen)

@@ -573,13 +573,14 @@ def moe_kv4_read(slots, cache: Kv4Cache, k_out=None, v_out=None, ws=None, stream
     return k_out, v_out
 
 
-def moe_kv4_attention(q, cache: Kv4Cache, page_table, lens, cu_q=None, max_q: int = 1, scale=None, out=None,
+def moe_kv4_attention(q, cache: Kv4Cache, page_table, lens, cu_q=None, max_q=None, scale=None, out=None,
                       lse=None, ws=None, stream=None):
     """Causal attention of q [T, Hq, D] (bf16, views allowed) over the 4-bit cache.
 
     Sequence b has the queries [cu_q[b], cu_q[b+1]) (cu_q int32 [B+1]; None: one each) and lens[b] keys
     (int32 [B]), the new tokens' own among them, in the pages page_table[b] (int32 [B, max_pages]).
-    max_q is the largest number of queries of a sequence. scale defaults to D ** -0.5.
+    max_q is the largest number of queries of a sequence: it chooses the kernel, never the result (None: 1
+    without cu_q, else the mean, rounded up; give it where the counts differ). scale defaults to D ** -0.5.
     ws: kv4_workspace(T, Hq, Hkv, D). Returns out, or (out, lse f32 [T, Hq]) where lse is given
     (a tensor, or True to have it made)."""
     c, Hkv, D = _cache(cache)
@@ -587,6 +588,8 @@ def moe_kv4_attention(q, cache: Kv4Cache, page_table, lens, cu_q=None, max_q: in
     B = lens.shape[0]
     at = _vec(lens, "lens", torch.int32)
     cu = None if cu_q is None else _vec(cu_q, "cu_q", torch.int32, B + 1)
+    if max_q is None:
+        max_q = 1 if cu is None else -(-T // max(B, 1))
     _need(page_table, "page_table", torch.int32, 2)
     if page_table.shape[0] != B:
         raise ValueError("page_table must have a row for each of the %d sequences, got %s" % (B, tuple(page_table.shape)))
