@@ -101,3 +101,26 @@ def test_max_q_left_out(calls, T, B, cu, given, chosen):
                           ws=_on(1 << 10, dtype=torch.uint8), **kw)
     args = calls["moe_kv4_attention"]
     assert args[7:11] == (B, T, 4, chosen)
+
+
+def _block_calls(ws):
+    cache, x, q = _fake_cache(), _on(3, 2, 128, dtype=torch.bfloat16), _on(3, 4, 128, dtype=torch.bfloat16)
+    slots = _on(3, dtype=torch.int32)
+    return (lambda: moe.moe_kv4_append(x, x, slots, cache, ws=ws),
+            lambda: moe.moe_kv4_read(slots, cache, x, x, ws=ws),
+            lambda: moe.moe_kv4_attention(q, cache, _on(3, 2, dtype=torch.int32), slots, out=q, ws=ws))
+
+
+def test_a_workspace_that_the_gpu_cannot_use_is_refused(calls):
+    """One in the host's memory, or strided, never reaches a kernel."""
+    for ws, error in ((torch.zeros(1 << 10, dtype=torch.uint8), ValueError), (_on(1 << 10, 2, dtype=torch.uint8)[:, 0], ValueError),
+                      (1 << 20, TypeError)):
+        for call in _block_calls(ws):
+            with pytest.raises(error):
+                call()
+    assert not calls
+    # its size is in bytes, whatever its type
+    ws = _on(1 << 10, dtype=torch.float32)
+    for call in _block_calls(ws):
+        call()
+    assert calls["moe_kv4_append"][7:9] == calls["moe_kv4_read"][5:7] == calls["moe_kv4_attention"][15:17] == (ws.data_ptr(), 1 << 12)

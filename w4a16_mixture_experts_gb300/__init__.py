@@ -505,6 +505,15 @@ def _vec(t, name, dtype, n=None):
     return t.data_ptr()
 
 
+def _ws_bytes(ws):
+    """(address, bytes) of a workspace."""
+    if type(ws) is not _Tensor and not isinstance(ws, _Tensor):
+        raise TypeError("ws must be a torch.Tensor")
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous CUDA tensor")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _cache(c):
     """(C struct, KV heads, D) of a Kv4Cache, or of four tensors in its order."""
     return (c if isinstance(c, Kv4Cache) else Kv4Cache(*c)).c()
@@ -549,7 +558,7 @@ def moe_kv4_append(k, v, slots, cache: Kv4Cache, ws=None, stream=None):
     if ws is None:
         ws = kv4_workspace(device=k.device)
     _check(lib().moe_kv4_append(k.data_ptr(), ks, v.data_ptr(), vs, _vec(slots, "slots", torch.int32, T), T, c,
-                                ws.data_ptr(), ws.numel(), _stream(stream)), "moe_kv4_append")
+                                *_ws_bytes(ws), _stream(stream)), "moe_kv4_append")
     return cache
 
 
@@ -568,7 +577,7 @@ def moe_kv4_read(slots, cache: Kv4Cache, k_out=None, v_out=None, ws=None, stream
             raise ValueError("%s must be %s, got %s" % (name, shape, tuple(t.shape)))
     if ws is None:
         ws = kv4_workspace(device=slots.device)
-    _check(lib().moe_kv4_read(at, shape[0], c, k_out.data_ptr(), v_out.data_ptr(), ws.data_ptr(), ws.numel(),
+    _check(lib().moe_kv4_read(at, shape[0], c, k_out.data_ptr(), v_out.data_ptr(), *_ws_bytes(ws),
                               _stream(stream)), "moe_kv4_read")
     return k_out, v_out
 
@@ -585,8 +594,8 @@ def moe_kv4_attention(q, cache: Kv4Cache, page_table, lens, cu_q=None, max_q=Non
     (a tensor, or True to have it made)."""
     c, Hkv, D = _cache(cache)
     qs, (T, Hq, _) = _heads(q, "q", None, None, D)
-    B = lens.shape[0]
     at = _vec(lens, "lens", torch.int32)
+    B = lens.shape[0]
     cu = None if cu_q is None else _vec(cu_q, "cu_q", torch.int32, B + 1)
     if max_q is None:
         max_q = 1 if cu is None else -(-T // max(B, 1))
@@ -606,7 +615,7 @@ def moe_kv4_attention(q, cache: Kv4Cache, page_table, lens, cu_q=None, max_q=Non
         ws = kv4_workspace(T, Hq, Hkv, D, device=q.device)
     _check(lib().moe_kv4_attention(q.data_ptr(), qs, c, page_table.data_ptr(), page_table.shape[1], at, cu, B, T, Hq,
                                    max_q, D ** -0.5 if scale is None else scale, out.data_ptr(), os_,
-                                   None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
+                                   None if lse is None else lse.data_ptr(), *_ws_bytes(ws),
                                    _stream(stream)), "moe_kv4_attention")
     return out if lse is None else (out, lse)
 
