@@ -505,6 +505,14 @@ def _vec(t, name, dtype, n=None):
     return t.data_ptr()
 
 
+def _made_on(stream):
+    """Outputs and workspaces that a call makes belong to the stream that it runs on: their clears come before the
+    kernels, and their memory is not given to another stream's tensors while the kernels run."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
 def _ws_bytes(ws):
     """(address, bytes) of a workspace."""
     if type(ws) is not _Tensor and not isinstance(ws, _Tensor):
@@ -528,6 +536,9 @@ def moe_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, ep
     positions int32 [T], inv_freq f32 [rot/2] (both None: norms alone), weights bf16 [D] or None.
     The pairs are (i, i + rot/2), or (2i, 2i + 1) with interleaved. Returns (q_out, k_out).
     """
+    if stream is not None and (q_out is None or k_out is None):
+        with _made_on(stream):
+            return moe_qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, q_out, k_out)
     qs, (T, Hq, D) = _heads(q, "q")
     ks, (_, Hkv, _) = _heads(k, "k", T, None, D)
     if q_out is None:
@@ -552,6 +563,9 @@ def moe_kv4_append(k, v, slots, cache: Kv4Cache, ws=None, stream=None):
     """Quantises token t's rows k[t], v[t] (bf16 [T, Hkv, D], views allowed) into the cache at
     slots[t] (int32 [T]; -1: not stored). ws: kv4_workspace(), whose error word
     moe_check_device_error reads. Returns the cache."""
+    if stream is not None and ws is None:
+        with _made_on(stream):
+            return moe_kv4_append(k, v, slots, cache)
     c, Hkv, D = _cache(cache)
     ks, (T, _, _) = _heads(k, "k", None, Hkv, D)
     vs = _heads(v, "v", T, Hkv, D)[0]
@@ -564,6 +578,9 @@ def moe_kv4_append(k, v, slots, cache: Kv4Cache, ws=None, stream=None):
 
 def moe_kv4_read(slots, cache: Kv4Cache, k_out=None, v_out=None, ws=None, stream=None):
     """The cache's rows at slots (int32 [T]; -1 reads as zero) as bf16 values: (k, v) [T, Hkv, D]."""
+    if stream is not None and (k_out is None or v_out is None or ws is None):
+        with _made_on(stream):
+            return moe_kv4_read(slots, cache, k_out, v_out, ws)
     c, Hkv, D = _cache(cache)
     at = _vec(slots, "slots", torch.int32)
     shape = (slots.shape[0], Hkv, D)
@@ -592,6 +609,9 @@ def moe_kv4_attention(q, cache: Kv4Cache, page_table, lens, cu_q=None, max_q=Non
     without cu_q, else the mean, rounded up; give it where the counts differ). scale defaults to D ** -0.5.
     ws: kv4_workspace(T, Hq, Hkv, D). Returns out, or (out, lse f32 [T, Hq]) where lse is given
     (a tensor, or True to have it made)."""
+    if stream is not None and (out is None or lse is True or ws is None):
+        with _made_on(stream):
+            return moe_kv4_attention(q, cache, page_table, lens, cu_q, max_q, scale, out, lse, ws)
     c, Hkv, D = _cache(cache)
     qs, (T, Hq, _) = _heads(q, "q", None, None, D)
     at = _vec(lens, "lens", torch.int32)
