@@ -58,3 +58,25 @@ def test_a_batch_of_no_tokens():
         assert moe.moe_kv4_attention(q, cache, i32(0, 4), i32(0), ws=ws).shape == (0, 8, 128)
         moe.moe_kv4_append(q[:, :2], q[:, :2], i32(0), cache, ws=ws)
         assert moe.moe_kv4_read(i32(0), cache, ws=ws)[0].shape == (0, 2, 128)
+
+
+@pytest.mark.parametrize("nq", [1, 6, 140])
+def test_a_workspace_of_the_calls_own(nq):
+    """Only its control block is cleared: whatever lies in the rest, the results are those of a zeroed one."""
+    g = _gen(nq)
+    Hkv, G, D, S, n = 2, 4, 128, 16, 3000
+    cache = _filled(g, 200, Hkv, S, D)
+    table = _tables(g, [n], S, 200)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    q = _randn(g, nq, Hkv * G, D).bfloat16()
+    args = (q, cache, table, i32(n), i32(0, nq), nq)
+    want, lse = moe.moe_kv4_attention(*args, lse=True, ws=moe.kv4_workspace(nq, Hkv * G, Hkv, D))
+    size = moe.moe_kv4_workspace_size(nq, Hkv * G, Hkv, D)
+    for fill in (0xFF, 0x7F, 1):
+        ws = torch.full((size,), fill, dtype=torch.uint8, device="cuda")
+        at = ws.data_ptr()
+        del ws                                            # the call gets this memory
+        got, z = moe.moe_kv4_attention(*args, lse=True)
+        again = torch.empty(size, dtype=torch.uint8, device="cuda")
+        assert again.data_ptr() == at and bool((again[256:512] == fill).all())
+        assert torch.equal(got, want) and torch.equal(z, lse)

@@ -631,8 +631,9 @@ def moe_kv4_attention(q, cache: Kv4Cache, page_table, lens, cu_q=None, max_q=Non
         _need(lse, "lse", _F32, 2)
         if lse.shape != (T, Hq):
             raise ValueError("lse must be [%d, %d], got %s" % (T, Hq, tuple(lse.shape)))
-    if ws is None:
-        ws = kv4_workspace(T, Hq, Hkv, D, device=q.device)
+    if ws is None:   # for this call alone: of what the call leaves zero it uses the control block only
+        ws = torch.empty(moe_kv4_workspace_size(T, Hq, Hkv, D), dtype=torch.uint8, device=q.device)
+        ws[:256].zero_()
     _check(lib().moe_kv4_attention(q.data_ptr(), qs, c, page_table.data_ptr(), page_table.shape[1], at, cu, B, T, Hq,
                                    max_q, D ** -0.5 if scale is None else scale, out.data_ptr(), os_,
                                    None if lse is None else lse.data_ptr(), *_ws_bytes(ws),
