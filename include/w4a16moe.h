@@ -401,7 +401,11 @@ MOE_API int moe_kv4_workspace_size(int32_t T, int32_t Hq, int32_t Hkv, int32_t D
  * A page outside [0, n_pages), a length outside [0, max_pages * page_size] and
  * query offsets that do not rise within [0, T] set MOE_ERR_DEVICE: such a
  * page's rows read as zero, and the others are brought into their range. Rows
- * of out that no sequence covers are not written.
+ * of out that no sequence covers are not written. Work is counted in units of
+ * 128 keys of one KV head for up to 8, 16 or 32 query rows of a sequence (256
+ * where max_q chooses the kernel for many), and 3 or 4 more for each such group
+ * of rows: a call of 2^31 units or more sets MOE_ERR_DEVICE too and writes
+ * nothing (a million queries behind a million keys on 128 KV heads; split it).
  *
  * The workspace holds moe_kv4_workspace_size() bytes under the rules of the
  * MoE calls (all zero before its first use); it may be one that they use.

@@ -80,3 +80,20 @@ def test_a_workspace_of_the_calls_own(nq):
         again = torch.empty(size, dtype=torch.uint8, device="cuda")
         assert again.data_ptr() == at and bool((again[256:512] == fill).all())
         assert torch.equal(got, want) and torch.equal(z, lse)
+
+
+def test_more_work_than_a_call_counts():
+    """2^31 units of work: refused on the device, and nothing is written."""
+    Hkv, D, S, nq, pages = 128, 64, 1024, 1 << 15, 1024
+    cache = moe.kv4_cache(1, Hkv, S, D)
+    q = torch.zeros(nq, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 3.0)
+    ws = moe.kv4_workspace(nq, Hkv, Hkv, D)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = torch.zeros(1, pages, dtype=torch.int32, device="cuda")
+    # 4096 groups of 8 rows x 8192 units x 128 heads
+    moe.moe_kv4_attention(q, cache, table, i32(pages * S), cu_q=i32(0, nq), max_q=1, out=out, ws=ws)
+    assert moe.moe_check_device_error(ws) == 5 and bool((out == 3).all())
+    # and the workspace is as good as new
+    assert bool((moe.moe_kv4_attention(q[:4], cache, table, i32(4), cu_q=i32(0, 4), max_q=4, ws=ws) == 0).all())
+    assert moe.moe_check_device_error(ws) == 0

@@ -171,7 +171,7 @@ struct Shares {
     __device__ Shares(int units, int ctas) : U(units), C(ctas), q(units / ctas), r(units % ctas) {}
     __device__ int begin(int c) const { return q * c + r * c / C; }
     __device__ int holder(int u) const {   // the CTA whose share holds unit u
-        int c = (int)((float)u * (float)C / (float)U);
+        int c = min((int)((float)u * (float)C / (float)U), C - 1);   // (begin(C + 1) may pass 2^31)
         while (begin(c + 1) <= u) ++c;
         while (begin(c) > u) --c;
         return c;
