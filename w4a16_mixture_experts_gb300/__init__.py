@@ -413,10 +413,11 @@ class Kv4Cache:
     """One layer's paged 4-bit KV cache: codes int32 [pages, Hkv, page_size, D/8] (q + 8, eight to a
     word, lowest nibble first) and scales bf16 [pages, Hkv, page_size], of K and of V. The slot of a
     token is page * page_size + its place in the page. Iterates over its four tensors."""
-    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales")
+    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "_c")
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales):
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self._c = (None, None)
 
     def __iter__(self):
         return iter((self.k_codes, self.k_scales, self.v_codes, self.v_scales))
@@ -427,7 +428,7 @@ class Kv4Cache:
         kc, ks, vc, vs = self.k_codes, self.k_scales, self.v_codes, self.v_scales
         try:
             n, h, p, w = shape = kc.shape
-            rows = shape[:3]
+            rows = (n, h, p)
             good = (kc.dtype is _I32 and vc.dtype is _I32 and ks.dtype is _BF16 and vs.dtype is _BF16
                     and vc.shape == shape and ks.shape == rows and vs.shape == rows
                     and kc.is_cuda and ks.is_cuda and vc.is_cuda and vs.is_cuda
@@ -441,7 +442,10 @@ class Kv4Cache:
             _need(vs, "v_scales", torch.bfloat16, 3)
             raise ValueError("a cache holds codes [pages, Hkv, page_size, D/8] and scales [pages, Hkv, page_size], "
                              "got %s %s %s %s" % tuple(tuple(t.shape) for t in self))
-        return moe_kv4_cache(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), n, h, p, w * 8), h, w * 8
+        at = (kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), shape)
+        if self._c[0] != at:   # (forming the struct takes longer than finding that it holds these values)
+            self._c = at, moe_kv4_cache(*at[:4], n, h, p, w * 8)
+        return self._c[1], h, w * 8
 
 
 def kv4_cache(n_pages: int, Hkv: int, page_size: int, D: int, device=None) -> Kv4Cache:
@@ -519,7 +523,7 @@ def _ws_bytes(ws):
         raise TypeError("ws must be a torch.Tensor")
     if not ws.is_cuda or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous CUDA tensor")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.nbytes
 
 
 def _cache(c):
