@@ -345,7 +345,7 @@ typedef struct {
  *
  * q, q_out bf16 [T][Hq][D], k, k_out bf16 [T][Hkv][D] (an output may be its
  * input, with the same strides); q_weight, k_weight bf16 [D] or NULL (ones);
- * positions int32 [T]; inv_freq f32 [rot/2]. D is 64, 128 or 256; rot a
+ * positions int32 [T]; inv_freq f32 [rot/2], finite. D is 64, 128 or 256; rot a
  * multiple of 16 from 0 to D (0: norms alone; positions and inv_freq may be
  * NULL); Hq or Hkv may be 0.
  */
@@ -392,11 +392,17 @@ MOE_API int moe_kv4_workspace_size(int32_t T, int32_t Hq, int32_t Hkv, int32_t D
  * q, out bf16 [T][Hq][D] (out must not overlap q or the cache); lse f32
  * [T][Hq] or NULL. Hq is a multiple of Hkv with at most 32 query heads a KV
  * head; T <= 2^20, B <= 4096. max_q is the largest number of queries of a
- * sequence: it decides which kernel runs, never the result.
+ * sequence: it decides which kernel runs, never the result, but for the roundings
+ * that follow.
  *
- * Softmax statistics and sums are fp32; a probability is rounded to fp16 where
- * it feeds the tensor core, the codes enter it exactly, and out is rounded to
- * bf16 once.
+ * Softmax statistics and sums are fp32. Codes and scales enter the products
+ * exactly; a query's values do where they lie within 2^25 of its row's largest,
+ * and are rounded at 2^-33 of that otherwise. A probability (or its product with
+ * the key's V scale) is rounded to fp16 where it feeds the tensor core: by 2^-11
+ * of itself, or by 2^-31 of the row's largest where it is smaller than 2^-20 of
+ * that. A key counts by what it adds to a row: one that the row does not see, or
+ * that has no probability in it, takes nothing from the others, whatever its
+ * scales (which may lie 2^100 apart in a sequence). out is rounded to bf16 once.
  *
  * A page outside [0, n_pages), a length outside [0, max_pages * page_size] and
  * query offsets that do not rise within [0, T] set MOE_ERR_DEVICE: such a

@@ -25,8 +25,12 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxSeqs = 4096;       // of a call
 constexpr float kNoMax = -3e38f;   // below every score: nothing seen yet
 
-// Up to so many rows of a sequence share one streaming pass; more go to the
-// tensor core.
+// Up to so many rows of a sequence share one streaming pass; calls with more take
+// the kernel with two tiles of 128 rows. (4 KV heads x 8, D = 128, us there and here:
+// 24 sequences of 1400 to 2780 keys, 32 rows 38 and 52, 40 rows 49 and 52, 72 rows 70 and
+// 55; 96 of 400 to 800 keys, 32 rows 58 and 90, 40 rows 97 and 90; 4 of 15000 to 30000
+// keys, 32 rows 50 and 62, 40 rows 56 and 62, 72 rows 74 and 62. D = 64: 32 rows 29 and
+// 35, 50 and 57, 39 and 46; 40 rows 38 and 35, 85 and 57, 46 and 46.)
 constexpr int kDecodeRows = 32;
 constexpr int kPromptRows = 256;
 

@@ -12,7 +12,7 @@
 //   O^T (D x R) += V^T (D x 128 keys) . P^T: V and P go to shared memory as they
 //     are, a row a key (MN-major operands).
 // The codes come by cp.async, a warp its own 32 keys, a unit ahead of their use.
-// (Loads into registers measured 90-125 us where this takes 72: the waits for them
+// (Loads into registers measured 90-125 us where this took 72: the waits for them
 // are counted on few scoreboards, so that a shuffle or a shared load behind them
 // waited for them too; and a row a lane from global memory visits each cache line
 // four times, which had the L1 74% busy.) A warp-level form (mma.sync on fragments
@@ -25,7 +25,8 @@
 // which are rounded at 2^-33 of it. (With K as e4m3 codes q + 8, which take a third
 // of the instructions, and a query as two e4m3 numbers, what a value far above the
 // rest left of them was rounded at 2^-18 of it, and 8 times it passed through the
-// sums of keys that hold zeros beside it.)
+// sums of keys that hold zeros beside it. That took 71.5 us for two sequences of
+// 131072 keys, this 74.5.)
 // A V scale multiplies its key's probabilities just before they are rounded to
 // fp16, so what is rounded is what the key adds to the row. A row's exponents are
 // therefore taken off not against its largest score but against its largest
@@ -48,9 +49,10 @@ namespace {
 using namespace kv4;
 
 constexpr int kKeys = 128;   // keys of a unit: a warpgroup's turn
-// What an item's start and end count for, in units (96 sequences of 400 to 4001 keys, D = 128: 43.9,
-// 41.8, 40.4, 40.9 us with 1, 2, 3, 4; 24 of 833 to 2777 keys, 16 rows, D = 64: 26.8, 26.5, 25.0, 26.0
-// with 2, 3, 4, 6).
+// What an item's start and end count for, in units; it moves the balance, never a result. (96 sequences
+// of 427 to 3994 keys, 8 rows, D = 128: 44.7, 42.5, 41.7, 42.6 us with 1, 2, 3, 4, D = 64: 36.2, 34.6,
+// 34.7, 36.7 with 2, 3, 4, 6; 24 of 905 to 2757 keys, D = 64, 16 rows: 26.0, 25.7, 24.4, 25.5, 32 rows: 44.7,
+// 43.9, 42.2, 41.4; D = 128, 16 rows: 32.6, 31.6, 30.6, 29.9, 32 rows: 56.1, 54.9, 53.7, 51.6 with 1, 2, 3, 4.)
 template <int D>
 constexpr int kLead = D == 128 ? 3 : 4;
 

@@ -20,7 +20,7 @@
 // The softmax is on a tile's path between its two products, so it is what must be
 // short: the scores stay in registers (read twice from tensor memory, with 128
 // registers a thread, 4096 queries of 32 heads behind 12288 keys took 875 us, so 766;
-// with what follows they take 697, 73% of the tensor core's rate), and a stage is
+// with what follows 716, 71% of the tensor core's rate), and a stage is
 // 128 keys wide, because the scores' product reads the queries again for each of
 // its parts (64 keys wide, with the other 64 keys' softmax meanwhile: 924 us then).
 // S = Q K^T has both operands K-major in the 128-byte swizzle; O += P V takes V
@@ -40,7 +40,7 @@
 // What is rounded to fp16 for the second product is a probability against the row's
 // largest so far, at 2^7 to 2^15, so at 2^-32 of the largest at most (at 1, a tail of
 // 2^17 keys below 2^-25 was lost); with codes, its product with the V scale against
-// the row's largest such product.
+// the row's largest such product. (With every stage in codes the chunk of 4096 takes 1486 us.)
 #include "kv4_attention.cuh"
 #include "tcgen05.cuh"
 
@@ -61,8 +61,8 @@ constexpr int kStages = 2;
 // registers a thread after the split: 256 x 160 + 256 x 64 + 128 x 32 = 640 x 96
 constexpr int kRegsSoft = 160, kRegsDeq = 64, kRegsMma = 32, kRegsLaunch = 96;
 static_assert(256 * kRegsSoft + 256 * kRegsDeq + 128 * kRegsMma <= kThreads * kRegsLaunch, "register split");
-// What an item's start and end count for, in stages. (Ragged prompts, D = 64: 103.9 us with 2, 97.2
-// with 3, 98.0 with 4; the chunk of 4096, D = 128: 700.0, 697.0, 695.4.)
+// What an item's start and end count for, in stages. (Ragged prompts, D = 64: 108.8 us with 2, 102.8
+// with 3, 102.9 with 4; the chunk of 4096, D = 128: 719.7, 716.0, 715.6.)
 constexpr int kLead = 3;
 
 template <int D>
