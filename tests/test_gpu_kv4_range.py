@@ -265,3 +265,23 @@ def test_zero_scales_before_others(nq, max_q, then):
     cache.v_scales[page[700:], 0, at[700:]] *= 2.0 ** -20
     q = (1.6 * _randn(g, nq, G, D)).bfloat16()
     _near(q, cache, table, n, max_q, rows=sorted({0, nq // 2, nq - 1}), copies=700)
+
+
+@pytest.mark.parametrize("where", [0, 200, 900])
+@pytest.mark.parametrize("nq,max_q", [(1, 1), (6, 6), (140, 140)])
+def test_a_zero_row_that_has_all_the_probability(nq, max_q, where):
+    """A key 40 nats above the others holds zeros: what the others add, 2^-58 of their values, is all that there is."""
+    g = _gen(nq)
+    n, S, G, D = 1200, 16, 4, 128
+    cache, table, page, at = _one_sequence(g, n, S, D)
+    codes = (_randn(g, n, D) * 1.2).round().clamp(-8, 7)
+    codes[:, 0] = 0
+    codes[where, 0] = 7
+    cache.k_codes[page, 0, at] = _words(codes)
+    cache.k_scales.fill_(0.5)
+    cache.v_scales[page[where], 0, at[where]] = 0
+    if where == 200:                                     # and nothing but zeros before it
+        cache.v_scales[page[:200], 0, at[:200]] = 0
+    q = _randn(g, nq, G, D).bfloat16()
+    q[..., 0] = 40 / 3.5 * D ** 0.5
+    _near(q, cache, table, n, max_q, rows=sorted({0, nq // 2, nq - 1}), copies=700)

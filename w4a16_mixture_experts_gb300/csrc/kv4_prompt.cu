@@ -112,16 +112,17 @@ __device__ inline void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u3
 constexpr int kKeyRange = 16, kValueRange = 10;
 
 // The exponents of the scales so far, K's or V's of an item.
+constexpr int kNoExponent = 1 << 20;
+__device__ inline int exponent_of(float s, int zero) {   // (bf16 has 7 octaves below its smallest normal)
+    const int e = (int)(__float_as_uint(s) >> 23 & 0xFFu);
+    return s == 0.f ? zero : e == 0 ? -7 : e;
+}
 struct Range {
-    int top = 1, low = 1 << 20;
-    __device__ bool holds(float s) const {   // (a zero has none)
-        const int e = (int)(__float_as_uint(s) >> 23 & 0xFFu);
-        return s == 0.f || (e <= top && e >= low);
-    }
-    __device__ void take(float s, int *tops, int *lows, int w4, int lane) const {   // a warp's
-        const int e = (int)(__float_as_uint(s) >> 23 & 0xFFu);
-        const int t = (int)__reduce_max_sync(0xffffffffu, (uint32_t)e);
-        const int l = __reduce_min_sync(0xffffffffu, s == 0.f ? 1 << 20 : e == 0 ? -7 : e);   // (bf16 has 7 octaves below its smallest normal)
+    int top = 1, low = kNoExponent;
+    __device__ bool holds(int e) const { return e == kNoExponent || (e <= top && e >= low); }
+    __device__ static void take(int e, int *tops, int *lows, int w4, int lane) {   // a warp's
+        const int t = (int)__reduce_max_sync(0xffffffffu, (uint32_t)(e == kNoExponent ? 0 : max(e, 0)));
+        const int l = __reduce_min_sync(0xffffffffu, e);
         if (lane == 0) {
             tops[w4] = t;
             lows[w4] = l;
@@ -248,9 +249,10 @@ __device__ inline void codes_stage(float (&row)[3], uint32_t tS, uint32_t tO, co
         for (int j = 0; j < 32; ++j) big = fmaxf(big, x[j] + a.scales.by[i * 32 + j]);
     }
     if (__any_sync(0xffffffffu, !a.codes || big > m + 8.f || a.up)) {
-        // (from scores to products: what the row has may lie kValueRange below)
-        // (in halves: a sum of probabilities may lie far above 1, the factor below fp32's range)
-        const float mn = fmaxf(a.codes ? m : m - kValueRange, big), down = exp2_approx(0.5f * (m - mn));
+        // (from probabilities to products: the largest the row has may lie kValueRange below, or anywhere
+        // where all V rows were zeros. In halves: a sum of probabilities may lie far above 1, the
+        // factor below fp32's range)
+        const float mn = fmaxf(a.codes ? m : m - (a.up ? 90.f : (float)kValueRange), big), down = exp2_approx(0.5f * (m - mn));
         m = mn;
         l0 = l0 * down * down;
         l1 = l1 * down * down;
@@ -672,19 +674,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                 // ---- the exponents; a row that was not finite: K becomes NaN, V zero
                 const bool bad = !finite_bits(ks) || !finite_bits(vs);
                 const float kf = bad ? 0.f : bf16_bits_to_f32(ks), vf = bad ? 0.f : bf16_bits_to_f32(vs);
+                // (a row of zeros in V lies far below the others: its key may have all the probability)
+                const int ke = exponent_of(kf, kNoExponent), ve = exponent_of(vf, st * kKeys + r < len && !bad ? -100 : kNoExponent);
                 // (most stages change nothing: that is seen at the barrier alone. With four reductions a warp
                 // for each stage's own exponents the prompt chunk took 756 us, so 732; with the first stage's
                 // before the wait 850)
-                if (st == st0 || !bar_and(keys ? 2 : 3, 128, ok && k_range.holds(kf) && v_range.holds(vf))) {
+                if (st == st0 || !bar_and(keys ? 2 : 3, 128, ok && k_range.holds(ke) && v_range.holds(ve))) {
                     int(&red)[4][4] = s_red[!keys][g & 1];   // (a stage has a barrier at least: the last stage's may still be read)
-                    k_range.take(kf, red[0], red[1], w4, lane);
-                    v_range.take(vf, red[2], red[3], w4, lane);
+                    Range::take(ke, red[0], red[1], w4, lane);
+                    Range::take(ve, red[2], red[3], w4, lane);
                     if (!(ok = bar_and(keys ? 2 : 3, 128, ok))) break;   // (for all warps of the role at once)
                     k_range.join(red[0], red[1]);
                     v_range.join(red[2], red[3]);
                     // (with codes V's exponent stays, as a middle for their range)
                     if (!codes) {
-                        codes = k_range.low < k_range.top - kKeyRange || v_range.low < v_range.top - kValueRange;
+                        // (V all zeros so far: none is lost to another)
+                        codes = k_range.low < k_range.top - kKeyRange || (v_range.top > 1 && v_range.low < v_range.top - kValueRange);
                         if (!codes || F == 1) F = min(v_range.top, 253);
                         E = codes ? 0 : min(k_range.top, 253);
                     }
