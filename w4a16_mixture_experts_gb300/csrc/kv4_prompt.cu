@@ -32,7 +32,7 @@
 // its range: K and V rows are less the exponent of the largest K or V scale so far
 // (K's put back in fp32 in the scores, V's at the end; the sums are rescaled when
 // it grows). From the stage on where the K scales so far lie more than 2^16 apart
-// (kKeyRange), or the V scales more than 2^10 (kValueRange), the rows are the codes alone,
+// (kKeyRange), or the V scales more than 2^10 (kValueRange; zeros too), the rows are the codes alone,
 // and the softmax multiplies scores and probabilities by the keys' scales in fp32: a
 // key that a row does not see, or that has no probability in it, takes nothing from
 // the others. A query row enters less its own exponent, its largest value brought
