@@ -283,6 +283,28 @@ MOE_API int moe_w8a16_linear(const uint16_t *x, const int32_t *w_packed, const u
 MOE_API int moe_w8a16_workspace_size(int32_t T, int32_t N, int32_t K, int32_t gs, size_t *bytes);
 
 /*
+ * W4A16 linear layer (no counterpart on the pages, whose INT4 weights are the
+ * experts' alone): y = x . W^T with a matrix in the experts' storage, as
+ * moe_quantize_int4 writes it:
+ *   W[n][c] = (nibble c%8 of w_packed[n][c/8] - 8) * scales[n][c/128]
+ *   y[t][n] = sum_c x[t][c] * W[n][c]
+ * x bf16 [T][K]; w_packed int32 [N][K/8]; scales bf16 [N][K/128]; y bf16 [T][N]
+ * (output; must not overlap an input). K is a multiple of 128, at most 65536;
+ * T <= 2^20. Codes enter the products exactly, sums are fp32 and each group's is
+ * multiplied by its scale in fp32; y is rounded to bf16 once. A scale or a value
+ * of x that is not finite reaches the values of y that it belongs to, and no others.
+ * The order of the sums depends on T, N, K and the device alone.
+ * ws: moe_w4a16_workspace_size() bytes under the rules of the MoE calls (it may
+ * be one that they use); a bounded wait that gave up sets MOE_ERR_TIMEOUT in it.
+ * T = 0 or N = 0 return MOE_OK with nothing enqueued.
+ */
+MOE_API int moe_w4a16_linear(const uint16_t *x, const int32_t *w_packed, const uint16_t *scales, uint16_t *y, int32_t T,
+                     int32_t N, int32_t K, void *ws, size_t ws_bytes, void *stream);
+
+/* Workspace bytes moe_w4a16_linear needs for these dims (256 at least). */
+MOE_API int moe_w4a16_workspace_size(int32_t T, int32_t N, int32_t K, size_t *bytes);
+
+/*
  * INT4 quantiser of BF16 weights into the experts' storage ("vLLM
  * Optimization Edition", section 7 "Putting MTP on the GPU", make_mtp_int4.py:
  * round to nearest, group size 128, symmetric, per-group search for the clip

@@ -26,6 +26,7 @@ __all__ = [
     "moe_pack_int4", "moe_quantize_int4", "moe_w8a16_linear", "moe_w8a16_workspace_size", "moe_check_device_error", "moe_profile_events", "moe_w4a16_forward_noalloc",
     "moe_noalloc_check_device_error", "moe_forward_plan", "STATUS", "Kv4Cache", "kv4_cache", "kv4_workspace",
     "moe_kv4_workspace_size", "moe_qk_norm_rope", "moe_kv4_append", "moe_kv4_read", "moe_kv4_attention",
+    "moe_w4a16_linear", "moe_w4a16_workspace_size",
 ]
 
 _DIR = os.path.dirname(os.path.abspath(__file__))
@@ -112,6 +113,9 @@ def lib() -> ctypes.CDLL:
         L.moe_kv4_workspace_size.restype = I
         L.moe_kv4_attention.argtypes = [P, S, C, P, I32, P, P, I32, I32, I32, I32, F, P, S, P, P, Z, P]
         L.moe_kv4_attention.restype = I
+        L.moe_w4a16_linear.argtypes, L.moe_w4a16_linear.restype = [P, P, P, P, I32, I32, I32, P, Z, P], I
+        L.moe_w4a16_workspace_size.argtypes = [I32, I32, I32, ctypes.POINTER(Z)]
+        L.moe_w4a16_workspace_size.restype = I
         _lib = L
     return _lib
 
@@ -643,6 +647,47 @@ def moe_kv4_attention(q, cache: Kv4Cache, page_table, lens, cu_q=None, max_q=Non
                                    None if lse is None else lse.data_ptr(), *_ws_bytes(ws),
                                    _stream(stream)), "moe_kv4_attention")
     return out if lse is None else (out, lse)
+
+
+def _mat(t, name, dtype, rows=None, cols=None):
+    """The address and shape of a contiguous CUDA matrix."""
+    if type(t) is not _Tensor and not isinstance(t, _Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    shape = t.shape
+    good = t.dtype is dtype and len(shape) == 2 and t.is_cuda and t.is_contiguous()
+    if not good or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
+        raise ValueError("%s must be a contiguous %s CUDA tensor [%s, %s], got %s %s" % (
+            name, dtype, "rows" if rows is None else rows, "columns" if cols is None else cols, t.dtype, tuple(shape)))
+    return t.data_ptr(), shape
+
+
+def moe_w4a16_workspace_size(T: int, N: int, K: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_w4a16_workspace_size(T, N, K, ctypes.byref(n)), "moe_w4a16_workspace_size")
+    return n.value
+
+
+def moe_w4a16_linear(x, w_packed, scales, y=None, ws=None, stream=None):
+    """bf16 y [T, N] = x . W^T for INT4 weights in the experts' storage (moe_quantize_int4's): w_packed
+    int32 [N, K/8] (q + 8, eight to a word, lowest nibble first), scales bf16 [N, K/128]. ws: a zeroed
+    uint8 tensor of moe_w4a16_workspace_size bytes (allocated here when not given), whose error word
+    moe_check_device_error reads."""
+    if stream is not None and (y is None or ws is None):
+        with _made_on(stream):
+            return moe_w4a16_linear(x, w_packed, scales, y, ws)
+    xp, (T, K) = _mat(x, "x", _BF16)
+    if K % 128:
+        raise ValueError("x must have a multiple of 128 columns, got %d" % K)
+    wp, (N, _) = _mat(w_packed, "w_packed", _I32, None, K // 8)
+    sp, _ = _mat(scales, "scales", _BF16, N, K // 128)
+    if y is None:
+        y = torch.empty(T, N, dtype=_BF16, device=x.device)
+    yp, _ = _mat(y, "y", _BF16, T, N)
+    if ws is None:   # for this call alone: of what the call leaves zero it uses the control block only
+        ws = torch.empty(moe_w4a16_workspace_size(T, N, K), dtype=torch.uint8, device=x.device)
+        ws[:256].zero_()
+    _check(lib().moe_w4a16_linear(xp, wp, sp, yp, T, N, K, *_ws_bytes(ws), _stream(stream)), "moe_w4a16_linear")
+    return y
 
 
 def moe_profile_events(before=None, after=None):

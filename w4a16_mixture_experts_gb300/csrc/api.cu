@@ -9,6 +9,7 @@
 #include "common.cuh"
 #include "kernels.cuh"
 #include "kv4_kernels.cuh"
+#include "step_kernels.cuh"
 #include "w4a16moe.h"
 
 namespace moe {
@@ -324,6 +325,26 @@ int moe_w8a16_workspace_size(int32_t T, int32_t N, int32_t K, int32_t gs, size_t
         if (S > 1) n += (size_t)S * T * N * 4;
     }
     *bytes = n;
+    return MOE_OK;
+}
+
+int moe_w4a16_linear(const uint16_t *x, const int32_t *w_packed, const uint16_t *scales, uint16_t *y, int32_t T,
+                     int32_t N, int32_t K, void *ws, size_t ws_bytes, void *stream) {
+    size_t need = 0;
+    const int rc = moe_w4a16_workspace_size(T, N, K, &need);
+    if (rc) return rc;
+    if (!ptr_ok(x, T == 0) || !ptr_ok(w_packed, N == 0) || !ptr_ok(scales, N == 0) || !ptr_ok(y, T == 0 || N == 0))
+        return MOE_ERR_INVALID_ARG;
+    if (!ws || !aligned16(ws)) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+    if (T == 0 || N == 0) return MOE_OK;
+    return cuda_status(launch_w4a16(x, w_packed, scales, y, T, N, K, ws, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_w4a16_workspace_size(int32_t T, int32_t N, int32_t K, size_t *bytes) {
+    if (!bytes || T < 0 || N < 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+    if (K % kGroup || T > (1 << 20) || K > 65536) return MOE_ERR_UNSUPPORTED;
+    *bytes = w4a16_workspace_bytes(T, N, K);
     return MOE_OK;
 }
 
