@@ -61,7 +61,7 @@ typedef enum {
     MOE_ERR_UNSUPPORTED = 2,  /* shape outside the supported set */
     MOE_ERR_WORKSPACE = 3,    /* workspace too small */
     MOE_ERR_CUDA = 4,         /* a CUDA runtime call or launch failed */
-    MOE_ERR_DEVICE = 5,       /* a kernel saw an expert id, slot, page or length out of range */
+    MOE_ERR_DEVICE = 5,       /* a kernel saw an expert id, slot, page, length, token or logit out of range */
     MOE_ERR_TIMEOUT = 6       /* a kernel's bounded wait gave up */
 } moe_status;
 
@@ -442,6 +442,53 @@ MOE_API int moe_kv4_attention(const uint16_t *q, moe_strides q_strides, moe_kv4_
                       const int32_t *page_table, int32_t max_pages, const int32_t *lens, const int32_t *cu_q,
                       int32_t B, int32_t T, int32_t Hq, int32_t max_q, float scale,
                       uint16_t *out, moe_strides out_strides, float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Verification of drafted tokens against the target's probabilities (no
+ * counterpart on the pages, whose drafting stays with the serving engine).
+ *
+ * Sequence b has the rows [cu_rows[b], cu_rows[b+1]) (cu_rows int32 [B+1]) of
+ * logits: its drafts' and one more. Row i predicts the token after the sequence
+ * and its first i drafts; drafts[r] (int32 [T]) is the draft that stands at row r
+ * (the last row's entry is not read). With t = temperature[b] (f32 [B]; NULL: 1):
+ *   p = softmax(logits / t),  q = softmax(draft_logits / t), or 1 at the draft
+ *   and 0 elsewhere where draft_logits is NULL;
+ *   the draft x of row r is accepted while uniform[r] * q(x) < p(x);
+ *   at the first row that refuses its draft, the next token is the v with the
+ *   largest max(p_v - q_v, 0) / noise[b][v] (p_v / noise[b][v] where that is zero
+ *   for all), at the last row the v with the largest p_v / noise[b][v].
+ * With uniform from [0, 1) and noise from Exp(1) the tokens are distributed as if
+ * they had been drawn from the target alone. t = 0: a draft is accepted while it is
+ * the row's largest logit, which is the next token. Ties go to the lowest v.
+ *
+ * tokens int32 [T]: of each sequence its accepted drafts, the next token, then -1.
+ * accepted int32 [B]: the number of accepted drafts (0 for a sequence without rows).
+ *
+ * logits, draft_logits bf16 [T][V] with rows `stride` values apart (a multiple of
+ * 8); uniform f32 [T]; noise f32 [B][V], rows noise_stride (a multiple of 4)
+ * apart. V <= 2^20, T <= 65536, B <= 4096. A logit of -inf is a token of
+ * probability zero. noise below 2^-126 (NaN too) counts as 2^-126.
+ *
+ * Exponentials are fp32 in the rows' sums, whose error is a few 2^-24 of themselves;
+ * what is compared is formed in 64 bits. The result depends on the arguments alone.
+ *
+ * These set MOE_ERR_DEVICE, where the definition reaches them: a NaN, a +inf or
+ * nothing but -inf in a row of logits or draft logits, and a temperature that is
+ * negative or not finite (the next token is then -1); a draft outside [0, V) (it is
+ * refused, and takes nothing from p where draft_logits is NULL); offsets that do not
+ * rise within [0, T] (brought into their range). Rows of tokens that no sequence
+ * has are not written.
+ *
+ * ws: moe_verify_workspace_size() bytes under the rules of the MoE calls; it may
+ * be one that they use.
+ */
+MOE_API int moe_verify_drafts(const uint16_t *logits, int64_t logits_stride, const uint16_t *draft_logits,
+                      int64_t draft_stride, const int32_t *drafts, const int32_t *cu_rows, const float *temperature,
+                      const float *uniform, const float *noise, int64_t noise_stride, int32_t B, int32_t T, int32_t V,
+                      int32_t *tokens, int32_t *accepted, void *ws, size_t ws_bytes, void *stream);
+
+/* Workspace bytes moe_verify_drafts needs for these dims. */
+MOE_API int moe_verify_workspace_size(int32_t B, int32_t T, int32_t V, size_t *bytes);
 
 /*
  * Which kernels a forward call of dims `d` runs (a host-only query, no

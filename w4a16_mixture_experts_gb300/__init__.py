@@ -26,7 +26,7 @@ __all__ = [
     "moe_pack_int4", "moe_quantize_int4", "moe_w8a16_linear", "moe_w8a16_workspace_size", "moe_check_device_error", "moe_profile_events", "moe_w4a16_forward_noalloc",
     "moe_noalloc_check_device_error", "moe_forward_plan", "STATUS", "Kv4Cache", "kv4_cache", "kv4_workspace",
     "moe_kv4_workspace_size", "moe_qk_norm_rope", "moe_kv4_append", "moe_kv4_read", "moe_kv4_attention",
-    "moe_w4a16_linear", "moe_w4a16_workspace_size",
+    "moe_w4a16_linear", "moe_w4a16_workspace_size", "moe_verify_drafts", "moe_verify_workspace_size", "verify_workspace",
 ]
 
 _DIR = os.path.dirname(os.path.abspath(__file__))
@@ -116,6 +116,9 @@ def lib() -> ctypes.CDLL:
         L.moe_w4a16_linear.argtypes, L.moe_w4a16_linear.restype = [P, P, P, P, I32, I32, I32, P, Z, P], I
         L.moe_w4a16_workspace_size.argtypes = [I32, I32, I32, ctypes.POINTER(Z)]
         L.moe_w4a16_workspace_size.restype = I
+        L.moe_verify_drafts.argtypes = [P, I64, P, I64, P, P, P, P, P, I64, I32, I32, I32, P, P, P, Z, P]
+        L.moe_verify_drafts.restype = I
+        L.moe_verify_workspace_size.argtypes, L.moe_verify_workspace_size.restype = [I32, I32, I32, ctypes.POINTER(Z)], I
         _lib = L
     return _lib
 
@@ -688,6 +691,67 @@ def moe_w4a16_linear(x, w_packed, scales, y=None, ws=None, stream=None):
         ws[:256].zero_()
     _check(lib().moe_w4a16_linear(xp, wp, sp, yp, T, N, K, *_ws_bytes(ws), _stream(stream)), "moe_w4a16_linear")
     return y
+
+
+def moe_verify_workspace_size(B: int, T: int, V: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_verify_workspace_size(B, T, V, ctypes.byref(n)), "moe_verify_workspace_size")
+    return n.value
+
+
+def verify_workspace(B: int, T: int, V: int, device=None) -> torch.Tensor:
+    """A zeroed uint8 workspace of moe_verify_workspace_size bytes."""
+    return torch.zeros(moe_verify_workspace_size(B, T, V), dtype=torch.uint8, device=device if device is not None else "cuda")
+
+
+def _wide(t, name, dtype, rows=None, cols=None):
+    """Address, row stride and shape of a CUDA matrix with contiguous rows (a view of a wider one, say)."""
+    if type(t) is not _Tensor and not isinstance(t, _Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    shape = t.shape
+    good = t.dtype is dtype and len(shape) == 2 and t.is_cuda and (rows is None or shape[0] == rows) and (cols is None or shape[1] == cols)
+    if good:
+        n, m = shape
+        stride, one = t.stride()
+        good = one == 1 or m <= 1
+    if not good:
+        raise ValueError("%s must be a %s CUDA tensor [%s, %s] with contiguous rows, got %s %s" % (
+            name, dtype, "rows" if rows is None else rows, "columns" if cols is None else cols, t.dtype, tuple(shape)))
+    return t.data_ptr(), stride if n > 1 else 0, shape
+
+
+def moe_verify_drafts(logits, drafts, cu_rows, uniform, noise, draft_logits=None, temperature=None, tokens=None,
+                      accepted=None, ws=None, stream=None):
+    """Which drafted tokens the target accepts, and the token after them.
+
+    Sequence b has the rows [cu_rows[b], cu_rows[b+1]) (int32 [B+1]) of logits (bf16 [T, V], rows a multiple of 8
+    values apart): its drafts' and one more. drafts int32 [T] (the draft at each row; a last row's is not read);
+    uniform f32 [T] from [0, 1); noise f32 [B, V] from Exp(1) (rows a multiple of 4 apart); draft_logits as logits,
+    or None where the drafts were not drawn from probabilities; temperature f32 [B] (0: the largest logit; None: 1).
+    ws: verify_workspace(B, T, V). Returns (tokens int32 [T]: the accepted drafts, the next token, then -1;
+    accepted int32 [B])."""
+    if stream is not None and (tokens is None or accepted is None or ws is None):
+        with _made_on(stream):
+            return moe_verify_drafts(logits, drafts, cu_rows, uniform, noise, draft_logits, temperature, tokens, accepted, ws)
+    lp, ls, (T, V) = _wide(logits, "logits", _BF16)
+    dp, ds = (None, 0) if draft_logits is None else _wide(draft_logits, "draft_logits", _BF16, T, V)[:2]
+    cu = _vec(cu_rows, "cu_rows", _I32)
+    B = cu_rows.shape[0] - 1
+    if B < 0:
+        raise ValueError("cu_rows must hold an offset for each sequence and one more")
+    ep, es = _wide(noise, "noise", _F32, B, V)[:2]
+    if tokens is None:
+        tokens = torch.empty(T, dtype=_I32, device=logits.device)
+    if accepted is None:
+        accepted = torch.empty(B, dtype=_I32, device=logits.device)
+    if ws is None:   # for this call alone: of what the call leaves zero it uses the control block only
+        ws = torch.empty(moe_verify_workspace_size(B, T, V), dtype=torch.uint8, device=logits.device)
+        ws[:256].zero_()
+    _check(lib().moe_verify_drafts(lp, ls, dp, ds, _vec(drafts, "drafts", _I32, T), cu,
+                                   None if temperature is None else _vec(temperature, "temperature", _F32, B),
+                                   _vec(uniform, "uniform", _F32, T), ep, es, B, T, V, _vec(tokens, "tokens", _I32, T),
+                                   _vec(accepted, "accepted", _I32, B), *_ws_bytes(ws), _stream(stream)), "moe_verify_drafts")
+    return tokens, accepted
 
 
 def moe_profile_events(before=None, after=None):

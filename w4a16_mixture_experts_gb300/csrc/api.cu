@@ -146,7 +146,7 @@ const char *moe_status_str(int status) {
         case MOE_ERR_UNSUPPORTED: return "unsupported shape";
         case MOE_ERR_WORKSPACE: return "workspace too small";
         case MOE_ERR_CUDA: return "CUDA runtime or launch error";
-        case MOE_ERR_DEVICE: return "a kernel saw an expert id, slot, page or length out of range";
+        case MOE_ERR_DEVICE: return "a kernel saw an expert id, slot, page, length, token or logit out of range";
         case MOE_ERR_TIMEOUT: return "a kernel's bounded wait gave up";
         default: return "unknown status";
     }
@@ -469,6 +469,39 @@ int moe_kv4_attention(const uint16_t *q, moe_strides q_strides, moe_kv4_cache ca
     return cuda_status(launch_kv4_attention(q, q_strides, cache, page_table, max_pages, lens, cu_q, B, T, Hq, max_q,
                                             scale, out, out_strides, lse, ws,
                                             reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_verify_workspace_size(int32_t B, int32_t T, int32_t V, size_t *bytes) {
+    if (!bytes || B < 0 || T < 0 || V <= 0) return MOE_ERR_INVALID_ARG;
+    if (B > 4096 || T > 65536 || V > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+    *bytes = verify_workspace_bytes(B, T, V);
+    return MOE_OK;
+}
+
+int moe_verify_drafts(const uint16_t *logits, int64_t logits_stride, const uint16_t *draft_logits, int64_t draft_stride,
+                      const int32_t *drafts, const int32_t *cu_rows, const float *temperature, const float *uniform,
+                      const float *noise, int64_t noise_stride, int32_t B, int32_t T, int32_t V, int32_t *tokens,
+                      int32_t *accepted, void *ws, size_t ws_bytes, void *stream) {
+    size_t need = 0;
+    const int rc = moe_verify_workspace_size(B, T, V, &need);
+    if (rc) return rc;
+    // rows of 16-byte pieces, a stride that a row fits
+    const auto rows_bad = [](int64_t stride, int rows, int V, int piece) {
+        return stride < 0 || stride % piece || (rows > 1 && stride < V);
+    };
+    if (rows_bad(logits_stride, T, V, 8) || (draft_logits && rows_bad(draft_stride, T, V, 8)) || rows_bad(noise_stride, B, V, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (!ptr_ok(logits, T == 0) || !ptr_ok(noise, B == 0) || (draft_logits && !aligned16(draft_logits)))
+        return MOE_ERR_INVALID_ARG;
+    if ((T > 0 && (!aligned4(drafts) || !aligned4(uniform) || !aligned4(tokens))) ||
+        (B > 0 && (!aligned4(cu_rows) || !aligned4(accepted))) || (reinterpret_cast<uintptr_t>(temperature) & 3u))
+        return MOE_ERR_INVALID_ARG;
+    if (!ws || !aligned16(ws)) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+    if (B == 0) return MOE_OK;
+    const VerifyArgs a{logits, draft_logits, logits_stride, draft_stride, noise_stride, drafts, cu_rows,
+                       temperature, uniform, noise, tokens, accepted};
+    return cuda_status(launch_verify(a, B, T, V, ws, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int moe_profile_events(void *before_experts, void *after_experts) {
