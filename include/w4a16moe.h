@@ -444,6 +444,24 @@ MOE_API int moe_kv4_attention(const uint16_t *q, moe_strides q_strides, moe_kv4_
                       uint16_t *out, moe_strides out_strides, float *lse, void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * The same with a sliding window and first keys that stay visible: the query at
+ * position i (the last of a sequence is at lens[b] - 1) sees the keys j <= i with
+ * j > i - window (itself and the window - 1 before it) or j < sinks. window >= 1,
+ * sinks >= 0; a window of at least max_pages * page_size is moe_kv4_attention.
+ *
+ * Only what some query of a (sequence, KV head)'s row tile sees is read, in runs of
+ * 16 keys, so the pages that lie wholly before the windows of a sequence's queries
+ * of this call (first keys aside) may be gone: their entries in page_table are not
+ * looked at. What else holds for moe_kv4_attention holds here, hidden keys counting
+ * as those that a query does not see: whatever lies in them changes nothing.
+ */
+MOE_API int moe_kv4_attention_window(const uint16_t *q, moe_strides q_strides, moe_kv4_cache cache,
+                             const int32_t *page_table, int32_t max_pages, const int32_t *lens, const int32_t *cu_q,
+                             int32_t B, int32_t T, int32_t Hq, int32_t max_q, float scale, int32_t window,
+                             int32_t sinks, uint16_t *out, moe_strides out_strides, float *lse, void *ws,
+                             size_t ws_bytes, void *stream);
+
+/*
  * Verification of drafted tokens against the target's probabilities (no
  * counterpart on the pages, whose drafting stays with the serving engine).
  *

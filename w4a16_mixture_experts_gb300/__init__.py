@@ -27,6 +27,7 @@ __all__ = [
     "moe_noalloc_check_device_error", "moe_forward_plan", "STATUS", "Kv4Cache", "kv4_cache", "kv4_workspace",
     "moe_kv4_workspace_size", "moe_qk_norm_rope", "moe_kv4_append", "moe_kv4_read", "moe_kv4_attention",
     "moe_w4a16_linear", "moe_w4a16_workspace_size", "moe_verify_drafts", "moe_verify_workspace_size", "verify_workspace",
+    "moe_kv4_attention_window",
 ]
 
 _DIR = os.path.dirname(os.path.abspath(__file__))
@@ -113,6 +114,8 @@ def lib() -> ctypes.CDLL:
         L.moe_kv4_workspace_size.restype = I
         L.moe_kv4_attention.argtypes = [P, S, C, P, I32, P, P, I32, I32, I32, I32, F, P, S, P, P, Z, P]
         L.moe_kv4_attention.restype = I
+        L.moe_kv4_attention_window.argtypes = [P, S, C, P, I32, P, P, I32, I32, I32, I32, F, I32, I32, P, S, P, P, Z, P]
+        L.moe_kv4_attention_window.restype = I
         L.moe_w4a16_linear.argtypes, L.moe_w4a16_linear.restype = [P, P, P, P, I32, I32, I32, P, Z, P], I
         L.moe_w4a16_workspace_size.argtypes = [I32, I32, I32, ctypes.POINTER(Z)]
         L.moe_w4a16_workspace_size.restype = I
@@ -623,6 +626,21 @@ def moe_kv4_attention(q, cache: Kv4Cache, page_table, lens, cu_q=None, max_q=Non
     if stream is not None and (out is None or lse is True or ws is None):
         with _made_on(stream):
             return moe_kv4_attention(q, cache, page_table, lens, cu_q, max_q, scale, out, lse, ws)
+    return _attention(q, cache, page_table, lens, cu_q, max_q, scale, out, lse, ws, stream, None, 0)
+
+
+def moe_kv4_attention_window(q, cache: Kv4Cache, page_table, lens, window: int, sinks: int = 0, cu_q=None, max_q=None,
+                             scale=None, out=None, lse=None, ws=None, stream=None):
+    """moe_kv4_attention with a sliding window: the query at position i sees the keys j <= i with j > i - window
+    or j < sinks. Pages that lie wholly before the windows of a sequence's queries (and hold no first keys)
+    may be gone: their entries in page_table are not looked at."""
+    if stream is not None and (out is None or lse is True or ws is None):
+        with _made_on(stream):
+            return moe_kv4_attention_window(q, cache, page_table, lens, window, sinks, cu_q, max_q, scale, out, lse, ws)
+    return _attention(q, cache, page_table, lens, cu_q, max_q, scale, out, lse, ws, stream, window, sinks)
+
+
+def _attention(q, cache, page_table, lens, cu_q, max_q, scale, out, lse, ws, stream, window, sinks):
     c, Hkv, D = _cache(cache)
     qs, (T, Hq, _) = _heads(q, "q", None, None, D)
     at = _vec(lens, "lens", torch.int32)
@@ -645,10 +663,13 @@ def moe_kv4_attention(q, cache: Kv4Cache, page_table, lens, cu_q=None, max_q=Non
     if ws is None:   # for this call alone: of what the call leaves zero it uses the control block only
         ws = torch.empty(moe_kv4_workspace_size(T, Hq, Hkv, D), dtype=torch.uint8, device=q.device)
         ws[:256].zero_()
-    _check(lib().moe_kv4_attention(q.data_ptr(), qs, c, page_table.data_ptr(), page_table.shape[1], at, cu, B, T, Hq,
-                                   max_q, D ** -0.5 if scale is None else scale, out.data_ptr(), os_,
-                                   None if lse is None else lse.data_ptr(), *_ws_bytes(ws),
-                                   _stream(stream)), "moe_kv4_attention")
+    args = (q.data_ptr(), qs, c, page_table.data_ptr(), page_table.shape[1], at, cu, B, T, Hq, max_q,
+            D ** -0.5 if scale is None else scale)
+    rest = (out.data_ptr(), os_, None if lse is None else lse.data_ptr(), *_ws_bytes(ws), _stream(stream))
+    if window is None:
+        _check(lib().moe_kv4_attention(*args, *rest), "moe_kv4_attention")
+    else:
+        _check(lib().moe_kv4_attention_window(*args, window, sinks, *rest), "moe_kv4_attention_window")
     return out if lse is None else (out, lse)
 
 

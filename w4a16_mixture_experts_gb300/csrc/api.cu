@@ -23,7 +23,7 @@ struct SmemAttr {
     int bytes;
     bool done[kMaxDevices];
 };
-constexpr int kMaxSmemKernels = 32;   // kernels that raise their shared-memory limit (20 today)
+constexpr int kMaxSmemKernels = 64;   // kernels that raise their shared-memory limit (30 today)
 SmemAttr g_attrs[kMaxSmemKernels];
 int g_nattrs = 0;
 std::mutex g_attrs_mu;   // callers may launch from several host threads
@@ -448,10 +448,11 @@ int moe_kv4_workspace_size(int32_t T, int32_t Hq, int32_t Hkv, int32_t D, size_t
     return MOE_OK;
 }
 
-int moe_kv4_attention(const uint16_t *q, moe_strides q_strides, moe_kv4_cache cache, const int32_t *page_table,
-                      int32_t max_pages, const int32_t *lens, const int32_t *cu_q, int32_t B, int32_t T, int32_t Hq,
-                      int32_t max_q, float scale, uint16_t *out, moe_strides out_strides, float *lse, void *ws,
-                      size_t ws_bytes, void *stream) {
+int moe_kv4_attention_window(const uint16_t *q, moe_strides q_strides, moe_kv4_cache cache, const int32_t *page_table,
+                             int32_t max_pages, const int32_t *lens, const int32_t *cu_q, int32_t B, int32_t T,
+                             int32_t Hq, int32_t max_q, float scale, int32_t window, int32_t sinks, uint16_t *out,
+                             moe_strides out_strides, float *lse, void *ws, size_t ws_bytes, void *stream) {
+    if (window < 1 || sinks < 0) return MOE_ERR_INVALID_ARG;
     int rc = check_cache(cache);
     if (rc) return rc;
     size_t need = 0;
@@ -466,9 +467,19 @@ int moe_kv4_attention(const uint16_t *q, moe_strides q_strides, moe_kv4_cache ca
     if (!ws || !aligned16(ws)) return MOE_ERR_INVALID_ARG;
     if (ws_bytes < need) return MOE_ERR_WORKSPACE;
     if (T == 0) return MOE_OK;
+    // a window (or first keys) that every length fits hides nothing
+    if (window >= max_pages * cache.page_size || sinks >= max_pages * cache.page_size) window = sinks = 0;
     return cuda_status(launch_kv4_attention(q, q_strides, cache, page_table, max_pages, lens, cu_q, B, T, Hq, max_q,
                                             scale, out, out_strides, lse, ws,
-                                            reinterpret_cast<cudaStream_t>(stream)));
+                                            reinterpret_cast<cudaStream_t>(stream), window, sinks));
+}
+
+int moe_kv4_attention(const uint16_t *q, moe_strides q_strides, moe_kv4_cache cache, const int32_t *page_table,
+                      int32_t max_pages, const int32_t *lens, const int32_t *cu_q, int32_t B, int32_t T, int32_t Hq,
+                      int32_t max_q, float scale, uint16_t *out, moe_strides out_strides, float *lse, void *ws,
+                      size_t ws_bytes, void *stream) {
+    return moe_kv4_attention_window(q, q_strides, cache, page_table, max_pages, lens, cu_q, B, T, Hq, max_q, scale,
+                                    INT32_MAX, 0, out, out_strides, lse, ws, ws_bytes, stream);
 }
 
 int moe_verify_workspace_size(int32_t B, int32_t T, int32_t V, size_t *bytes) {

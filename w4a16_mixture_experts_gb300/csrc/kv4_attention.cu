@@ -115,11 +115,12 @@ size_t kv4_workspace_bytes(int T, int Hq, int Hkv, int D) {
 cudaError_t launch_kv4_attention(const uint16_t *q, moe_strides qs, const moe_kv4_cache &c, const int32_t *table,
                                  int max_pages, const int32_t *lens, const int32_t *cu_q, int B, int T, int Hq,
                                  int max_q, float scale, uint16_t *out, moe_strides os, float *lse, void *ws,
-                                 cudaStream_t s) {
+                                 cudaStream_t s, int window, int sinks) {
     const int G = Hq / c.Hkv;
     const long long rows = (long long)(max_q < T ? max_q : T) * G;
     const Attn p{{table, lens, cu_q, B, T, max_pages, __builtin_ctz((unsigned)c.page_size)}, q, qs, os, c, out, lse,
-                 reinterpret_cast<Ctrl *>(ws), ws_at<Begun>(ws, kPartOff), ws_at<float>(ws, kPartOff + kMaxCtas * sizeof(Begun)), scale, Hq, G};
+                 reinterpret_cast<Ctrl *>(ws), ws_at<Begun>(ws, kPartOff), ws_at<float>(ws, kPartOff + kMaxCtas * sizeof(Begun)), scale, Hq, G,
+                 window, sinks};
     int R = kPromptRows, grid = 0;
     const cudaError_t err = rows <= kDecodeRows ? launch_kv4_decode(p, (int)rows, &R, &grid, s) : launch_kv4_prompt(p, &grid, s);
     if (err != cudaSuccess) return err;

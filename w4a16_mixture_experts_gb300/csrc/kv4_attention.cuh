@@ -60,6 +60,8 @@ struct Attn {
     float *part;        // [CTAs][2] x part_floats(R, D): a CTA's first part continues an item, its second begins one
     float scale;
     int Hq, G;
+    // (instantiations with kWindow only) query at position i sees the keys j <= i with j > i - window or j < sinks
+    int window, sinks;
 };
 
 // A part of an item: the exponent taken off each row's scores and the sum of its
@@ -119,20 +121,37 @@ __device__ inline int tile_keys(const Seq &s, int G, int R, int qt) {
     return min(max(s.len - s.nq + last + 1, 0), s.len);
 }
 
+// First key that the window of the query at position pos holds.
+__device__ inline int window_low(const Attn &p, int pos) { return pos >= p.window ? pos - p.window + 1 : 0; }
+
+// With a window, what lies between the units with first keys (sinks) and the one where
+// the window of the tile's first row begins is left out: units [0, head) of keys stay
+// where they are, those from head on lie `skip` units further.
+struct Gap {
+    int head, skip;
+    __device__ int key_unit(int u) const { return u < head ? u : u + skip; }
+};
+template <int kKeys>
+__device__ inline Gap tile_gap(const Attn &p, const Seq &s, int R, int qt) {
+    const int head = (int)(((unsigned)p.sinks + kKeys - 1) / kKeys);
+    return Gap{head, max(window_low(p, s.len - s.nq + qt * R / p.G) / kKeys - head, 0)};
+}
+
 // Units of keys of a sequence's row tile: at least one, so that rows that see no
 // key are written too.
-template <int kKeys>
-__device__ inline int tile_units(const Seq &s, int G, int R, int qt) {
-    return max(1, (tile_keys(s, G, R, qt) + kKeys - 1) / kKeys);
+template <int kKeys, bool kWindow>
+__device__ inline int tile_units(const Attn &p, const Seq &s, int R, int qt) {
+    const int all = (tile_keys(s, p.G, R, qt) + kKeys - 1) / kKeys;
+    return max(1, kWindow ? all - tile_gap<kKeys>(p, s, R, qt).skip : all);
 }
 
 // The units of a sequence's row tiles, leading ones included, by a whole warp for
 // one sequence.
-template <int kKeys, int kLead>
-__device__ long long tiles_units(const Seq &s, int G, int R) {
-    const int tiles = (s.nq * G + R - 1) / R;
+template <int kKeys, int kLead, bool kWindow>
+__device__ long long tiles_units(const Attn &p, const Seq &s, int R) {
+    const int tiles = (s.nq * p.G + R - 1) / R;
     long long m = 0;
-    for (int qt = threadIdx.x & 31; qt < tiles; qt += 32) m += tile_units<kKeys>(s, G, R, qt) + kLead;
+    for (int qt = threadIdx.x & 31; qt < tiles; qt += 32) m += tile_units<kKeys, kWindow>(p, s, R, qt) + kLead;
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) m += __shfl_xor_sync(0xffffffffu, m, x);
     return m;
@@ -142,16 +161,16 @@ __device__ long long tiles_units(const Seq &s, int G, int R) {
 // tiles take a warp each: in a CTA of several warpgroups they are shared out over
 // all warps through `mid` (12 prompts of up to 1500 queries: 99.2 us with one warp for
 // them, 98.0 so).
-template <int kThreads, int kKeys, int kLead>
+template <int kThreads, int kKeys, int kLead, bool kWindow>
 __device__ long long head_units(const Attn &p, const Seq &s, int R, long long *mid) {
     const int tiles = (s.nq * p.G + R - 1) / R, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long n = 0;
     if (tiles <= 2)
-        for (int qt = 0; qt < tiles; ++qt) n += tile_units<kKeys>(s, p.G, R, qt) + kLead;
+        for (int qt = 0; qt < tiles; ++qt) n += tile_units<kKeys, kWindow>(p, s, R, qt) + kLead;
     if (kThreads <= 128) {
         for (uint32_t many = __ballot_sync(0xffffffffu, tiles > 2); many; many &= many - 1) {
             const int src = __ffs(many) - 1;
-            const long long m = tiles_units<kKeys, kLead>(Seq{0, __shfl_sync(0xffffffffu, s.nq, src), __shfl_sync(0xffffffffu, s.len, src)}, p.G, R);
+            const long long m = tiles_units<kKeys, kLead, kWindow>(p, Seq{0, __shfl_sync(0xffffffffu, s.nq, src), __shfl_sync(0xffffffffu, s.len, src)}, R);
             if (lane == src) n = m;
         }
     } else if (__syncthreads_or(tiles > 2)) {
@@ -160,7 +179,7 @@ __device__ long long head_units(const Attn &p, const Seq &s, int R, long long *m
         for (int i = warp; i < kThreads; i += kThreads / 32) {
             const long long x = mid[i];
             if (x < 0) continue;
-            const long long m = tiles_units<kKeys, kLead>(Seq{0, (int)(x >> 32), (int)x}, p.G, R);
+            const long long m = tiles_units<kKeys, kLead, kWindow>(p, Seq{0, (int)(x >> 32), (int)x}, R);
             if (lane == 0) mid[i] = m;
         }
         __syncthreads();
@@ -190,11 +209,11 @@ struct Item {
 
 // The row tile of a sequence and head (whose units begin at `at`) that holds unit u; a
 // whole warp calls it.
-template <int kKeys, int kLead>
+template <int kKeys, int kLead, bool kWindow>
 __device__ void find_tile(const Attn &p, int R, int u, int at, Item &it) {
     const int tiles = (it.s.nq * p.G + R - 1) / R, lane = threadIdx.x & 31;
     for (int q0 = 0;; q0 += 32) {   // 32 at a time
-        const int n = q0 + lane < tiles ? tile_units<kKeys>(it.s, p.G, R, q0 + lane) + kLead : 0;
+        const int n = q0 + lane < tiles ? tile_units<kKeys, kWindow>(p, it.s, R, q0 + lane) + kLead : 0;
         int inc = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -218,7 +237,7 @@ __device__ void find_tile(const Attn &p, int R, int u, int at, Item &it) {
 // All threads call it; it begins and ends with a barrier or more, between which
 // `pre` is used where there are more than kThreads sequences. A total of 2^31
 // units is refused as a value out of range.
-template <int kThreads, int kKeys, int kLead>
+template <int kThreads, int kKeys, int kLead, bool kWindow>
 __device__ Shares first_item(const Attn &p, int R, int c, int *pre, long long *warp_sums, Item &shared, Item &it) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long total = 0, before = 0, per_head = 0, n = 0;
@@ -226,7 +245,7 @@ __device__ Shares first_item(const Attn &p, int R, int c, int *pre, long long *w
     for (int b0 = 0; b0 < p.b.B; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
         s = b < p.b.B ? seq_of(p.b, b, p.ctrl) : Seq{0, 0, 0};
-        per_head = head_units<kThreads, kKeys, kLead>(p, s, R, reinterpret_cast<long long *>(pre + kMaxSeqs));
+        per_head = head_units<kThreads, kKeys, kLead, kWindow>(p, s, R, reinterpret_cast<long long *>(pre + kMaxSeqs));
         n = per_head * p.c.Hkv;
         long long inc = n;
 #pragma unroll
@@ -280,7 +299,7 @@ __device__ Shares first_item(const Attn &p, int R, int c, int *pre, long long *w
         }
         if (look) {
             x.h = (u - at) / (int)per_head;
-            find_tile<kKeys, kLead>(p, R, u, at + x.h * (int)per_head, x);
+            find_tile<kKeys, kLead, kWindow>(p, R, u, at + x.h * (int)per_head, x);
             if (lane == 0) shared = x;
         }
     }
@@ -290,7 +309,7 @@ __device__ Shares first_item(const Attn &p, int R, int c, int *pre, long long *w
 }
 
 // The item after `it`, where there is one.
-template <int kKeys, int kLead>
+template <int kKeys, int kLead, bool kWindow>
 __device__ void next_item(const Attn &p, int R, Item &it) {
     it.first += it.span;
     if ((it.qt + 1) * R < it.s.nq * p.G) {
@@ -303,7 +322,7 @@ __device__ void next_item(const Attn &p, int R, Item &it) {
             while (it.s.nq == 0);
         }
     }
-    it.units = tile_units<kKeys>(it.s, p.G, R, it.qt);
+    it.units = tile_units<kKeys, kWindow>(p, it.s, R, it.qt);
     it.span = it.units + kLead;
 }
 

@@ -80,6 +80,7 @@ struct DecodeShared {
     long long sums[4];
     Item first;
     int lim[R], we[4];                          // we: exponents of the warps' largest V scales in the item's first unit
+    int low[R];                                 // (with a window) a row's first key in it
     uint32_t tmem;
 };
 
@@ -228,7 +229,7 @@ __device__ inline void reduce_rows(const float (&v)[R], float *to) {
     if ((lane & (32 / R - 1)) == 0) to[row] = x[0];
 }
 
-template <int D, int R>
+template <int D, int R, bool kWindow>
 __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kPerSm) kv4_decode_kernel(Attn p) {
     using Cfg = DecodeCfg<D, R>;
     extern __shared__ __align__(1024) uint8_t s_dyn[];
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
     }
     const int c = blockIdx.x;
     Item it;
-    const Shares shares = first_item<Cfg::kThreads, kKeys, kLead<D>>(p, R, c, s_pre, sh.sums, sh.first, it);
+    const Shares shares = first_item<Cfg::kThreads, kKeys, kLead<D>, kWindow>(p, R, c, s_pre, sh.sums, sh.first, it);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -276,13 +277,27 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
     // page (page sizes are multiples of 16): lane i knows the run of keys 16 (i / 16) ...
     constexpr uint32_t kNone = 0xffffffffu;   // no such keys, or a page that does not exist: they read as zero
     const int run = warp * 32 + (lane & 16);
+    // With a window: where the item's units lie, the first key in the window of its first row and of its last.
+    Gap gap{0, 0};
+    int low = 0, low_last = 0;
+    auto look = [&]() {
+        if (kWindow) {
+            gap = tile_gap<kKeys>(p, it.s, R, it.qt);
+            low = window_low(p, it.s.len - it.s.nq + it.qt * R / p.G);
+            low_last = window_low(p, it.s.len - it.s.nq + (min((it.qt + 1) * R, it.s.nq * p.G) - 1) / p.G);
+        }
+    };
+    look();
+    auto first_key = [&](int st) { return (kWindow ? gap.key_unit(st) : st) * kKeys; };
+    // (a run that no row sees is not read: its page may be gone)
+    auto in_reach = [&](int key) { return key < it.s.len && (!kWindow || key < p.sinks || key > low - 16); };
     auto page_of = [&](int st) {
-        const int key = st * kKeys + run;
-        return st < st1 && key < it.s.len ? ld_here(p.b.table + (size_t)it.b * p.b.max_pages + (key >> p.b.shift)) : -1;
+        const int key = first_key(st) + run;
+        return st < st1 && in_reach(key) ? ld_here(p.b.table + (size_t)it.b * p.b.max_pages + (key >> p.b.shift)) : -1;
     };
     auto place = [&](int st, int page) {   // the run's first row (row indexes are below 2^32 - 1)
-        const int key = st * kKeys + run;
-        if (st >= st1 || key >= it.s.len) return kNone;
+        const int key = first_key(st) + run;
+        if (st >= st1 || !in_reach(key)) return kNone;
         if ((unsigned)page >= (unsigned)p.c.n_pages) {
             set_error(p.ctrl, MOE_ERR_DEVICE);
             return kNone;
@@ -414,6 +429,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
                 const float cc = fabsf(p.scale) * kLog2e * pow2_biased(e) * (1.f / 256.f);
                 sh.c[r] = big < 0x7F80u ? cc : __uint_as_float(0x7fc00000u);   // a query that is not finite: NaN
                 sh.lim[r] = r < rows ? it.s.len - it.s.nq + qi + 1 : 0;
+                if (kWindow) sh.low[r] = window_low(p, it.s.len - it.s.nq + qi);
             }
         }
         fence_proxy_async_smem();
@@ -421,6 +437,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
         if (tid < R) sh.m[tid] = 0.f;   // (the first unit sets it)
         // every row sees the keys below `least`
         const int least = max(it.s.len - it.s.nq + it.qt * R / p.G + 1, 0);
+        // Up to this unit there may be rows that have seen no key yet: without a window the first (a row
+        // sees a prefix of the keys), with one also that where the last row's window begins, unless
+        // the share has first keys, which all see.
+        const int begins = kWindow && st0 >= gap.head ? max(st0, low_last / kKeys - gap.skip) : st0;
 
         float l[R];
 #pragma unroll
@@ -430,7 +450,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
         copies_wait<0>();   // (K; V belongs to the next group)
         __syncwarp();
         {
-            const float fv = at0 != kNone && st * kKeys + tid < it.s.len ? fabsf(bf16_bits_to_f32(sh.scales[warp][0][1][lane])) : 0.f;
+            const float fv = at0 != kNone && first_key(st) + tid < it.s.len ? fabsf(bf16_bits_to_f32(sh.scales[warp][0][1][lane])) : 0.f;
             const uint32_t e = fv > 0.f && fv < INFINITY ? max(__float_as_uint(fv) >> 23, 1u) : 0u, top = __reduce_max_sync(0xffffffffu, e);
             if (lane == 0) sh.we[warp] = (int)top;
         }
@@ -455,7 +475,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
             const bool more = st + 1 < st1;
             // ---- the key's scores, less the maxima in use. Scales: a row that was not finite
             // makes its scores NaN, its values zero
-            const int key = st * kKeys + tid;
+            const int key0 = first_key(st), key = key0 + tid;
             const bool there = at0 != kNone && key < it.s.len;
             float fk = there ? bf16_bits_to_f32(sh.scales[warp][slot][0][lane]) : 0.f;
             float fv = there ? bf16_bits_to_f32(sh.scales[warp][slot][1][lane]) : 0.f;
@@ -502,10 +522,16 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
                 }
             }
             copies_commit();
-            if ((st + 1) * kKeys > least) {
+            if (key0 + kKeys > least) {
 #pragma unroll
                 for (int r = 0; r < R; ++r)
                     if (key >= sh.lim[r]) s[r] = -INFINITY;
+            }
+            if (kWindow && key0 < low_last && key0 + kKeys > p.sinks) {
+                const bool hidden = key >= p.sinks;
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    if (hidden && key < sh.low[r]) s[r] = -INFINITY;
             }
             // ---- probabilities; where one times its V scale would pass 2^15, or itself 2^96, the warp
             // leaves them until the rows' exponents have followed (and in the first unit, which sets them)
@@ -513,7 +539,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
             float top = s[0];
 #pragma unroll
             for (int r = 1; r < R; ++r) top = fmaxf(top, s[r]);
-            const bool over = __any_sync(0xffffffffu, turn == 0 || top > fminf(15.f - log_f, 96.f));
+            const bool over = __any_sync(0xffffffffu, (kWindow ? st <= begins : turn == 0) || top > fminf(15.f - log_f, 96.f));
             const uint32_t p_at = Cfg::kPs == 2 ? (turn & 1) * Cfg::kP : 0;
             auto values_added = [&]() {   // the last unit's values are in the sums, and V and P free
                 if (turn > 0) {
@@ -565,12 +591,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     const float x = fmaxf(fmaxf(sh.wm[0][r], sh.wm[1][r]), fmaxf(sh.wm[2][r], sh.wm[3][r]));
-                    // (a row that sees no key of the first unit sees none of the later ones)
-                    up[r] = turn > 0 ? fmaxf(x, 0.f) : x == kNoMax ? 0.f : x;
+                    // a row that has seen no key yet takes what comes (without a window: one that sees none of
+                    // the first unit sees none of the later ones)
+                    const bool fresh = turn == 0 || (kWindow && st <= begins && st <= sh.low[r] / kKeys - gap.skip);
+                    up[r] = !fresh ? fmaxf(x, 0.f) : x == kNoMax ? 0.f : x;
                     if (tid == r) sh.m[r] += up[r];   // (all have read the old ones before the barriers)
                     s[r] -= up[r];
-                    // (turn 0: nothing to rescale, and one far below zero has no power of two)
-                    up[r] = turn > 0 ? exp2_approx(-0.5f * up[r]) : 1.f;
+                    // (fresh: nothing to rescale, and one far below zero has no power of two)
+                    up[r] = !fresh ? exp2_approx(-0.5f * up[r]) : 1.f;
                     l[r] = l[r] * up[r] * up[r];
                 }
                 if (turn > 0) {
@@ -612,8 +640,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
         const bool first_part = st0 == 0, whole = first_part && st1 == it.units;
         bool last_item = it.first + it.span >= u_end;
         if (!last_item) {
-            next_item<kKeys, kLead<D>>(p, R, it);
+            next_item<kKeys, kLead<D>, kWindow>(p, R, it);
             last_item = u_end - it.first <= kLead<D>;
+            look();
         }
         if (!last_item) {
             st0 = 0;
@@ -674,18 +703,18 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
     if (warp == 0) tc::dealloc(sh.tmem, Cfg::kCols);
 }
 
-template <int D, int R>
+template <int D, int R, bool kWindow>
 cudaError_t launch_one(const Attn &p, int *rows_at, int *grid_out, cudaStream_t s) {
     using Cfg = DecodeCfg<D, R>;
     constexpr size_t kBytes = Cfg::kSmem + sizeof(DecodeShared<R>);
     static_assert((kBytes + 1024) * Cfg::kPerSm <= 233472, "shared memory");
-    const cudaError_t err = set_smem_once(reinterpret_cast<const void *>(kv4_decode_kernel<D, R>), (int)kBytes);
+    const cudaError_t err = set_smem_once(reinterpret_cast<const void *>(kv4_decode_kernel<D, R, kWindow>), (int)kBytes);
     if (err != cudaSuccess) return err;
     int grid = Cfg::kPerSm * sm_count();
     if (grid > kMaxCtas) grid = kMaxCtas;
     *rows_at = R;
     *grid_out = grid;
-    return launch_pdl(kv4_decode_kernel<D, R>, dim3((unsigned)grid), Cfg::kThreads, kBytes, s, p);
+    return launch_pdl(kv4_decode_kernel<D, R, kWindow>, dim3((unsigned)grid), Cfg::kThreads, kBytes, s, p);
 }
 
 }  // namespace
@@ -693,7 +722,11 @@ cudaError_t launch_one(const Attn &p, int *rows_at, int *grid_out, cudaStream_t 
 cudaError_t launch_kv4_decode(const kv4::Attn &p, int rows, int *rows_at, int *grid, cudaStream_t s) {
     auto pick = [&](auto d) {
         constexpr int D = decltype(d)::value;
-        return rows <= 8 ? launch_one<D, 8>(p, rows_at, grid, s) : rows <= 16 ? launch_one<D, 16>(p, rows_at, grid, s) : launch_one<D, 32>(p, rows_at, grid, s);
+        auto with = [&](auto w) {
+            constexpr bool W = decltype(w)::value;
+            return rows <= 8 ? launch_one<D, 8, W>(p, rows_at, grid, s) : rows <= 16 ? launch_one<D, 16, W>(p, rows_at, grid, s) : launch_one<D, 32, W>(p, rows_at, grid, s);
+        };
+        return p.window ? with(std::true_type{}) : with(std::false_type{});
     };
     return p.c.D == 64 ? pick(std::integral_constant<int, 64>{}) : pick(std::integral_constant<int, 128>{});
 }

@@ -17,7 +17,7 @@ size_t kv4_workspace_bytes(int T, int Hq, int Hkv, int D);
 cudaError_t launch_kv4_attention(const uint16_t *q, moe_strides qs, const moe_kv4_cache &c, const int32_t *table,
                                  int max_pages, const int32_t *lens, const int32_t *cu_q, int B, int T, int Hq,
                                  int max_q, float scale, uint16_t *out, moe_strides os, float *lse, void *ws,
-                                 cudaStream_t s);
+                                 cudaStream_t s, int window = 0, int sinks = 0);   // window 0: all keys before a query
 
 // A launch that may start while the kernel ahead of it in the stream ends: the
 // kernel calls pdl_wait() before it reads or writes anything.

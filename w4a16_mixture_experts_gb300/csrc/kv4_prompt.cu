@@ -220,11 +220,12 @@ struct CodesStage {
     float c_row;
     int left, up;        // keys of the stage that the row sees; how far V's exponent has risen
     bool sums, codes;    // there are sums so far; they are of stages of codes
+    int low, sinks;      // (with a window) keys [sinks, low) of the stage are hidden from the row
 };
 
 // A thread's row (m, l0, l1), 32 keys at a time. Such stages come last in an item and have
 // a loop of their own: as a branch in the other one they cost all prompts 4-7%, in line or not.
-template <int D>
+template <int D, bool kWindow>
 __device__ inline void codes_stage(float (&row)[3], uint32_t tS, uint32_t tO, const CodesStage &a) {
     float m = row[0], l0 = row[1], l1 = row[2];
     auto scores = [&](int i, float (&x)[32]) {
@@ -238,6 +239,12 @@ __device__ inline void codes_stage(float (&row)[3], uint32_t tS, uint32_t tO, co
             x[j + 1] = j + 1 < left ? x[j + 1] * (k.y * a.c_row) : -INFINITY;
             x[j + 2] = j + 2 < left ? x[j + 2] * (k.z * a.c_row) : -INFINITY;
             x[j + 3] = j + 3 < left ? x[j + 3] * (k.w * a.c_row) : -INFINITY;
+        }
+        if (kWindow) {
+            const int low = a.low - i * 32, sinks = a.sinks - i * 32;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (j < low && j >= sinks) x[j] = -INFINITY;
         }
     };
     float big = -INFINITY;
@@ -303,7 +310,7 @@ __device__ inline uint8_t *chunk_at(uint8_t *tile, int row, int chunk) {   // 8 
     return tile + (chunk >> 3) * 16384 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
 }
 
-template <int D>
+template <int D, bool kWindow>
 __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
     using Cfg = PromptCfg<D>;
     extern __shared__ uint8_t s_dyn[];
@@ -356,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
     pdl_launch_dependents();
     const int c = blockIdx.x;
     Item it;
-    const Shares shares = first_item<kThreads, kKeys, kLead>(p, kR, c, s_pre, s_sums, s_first, it);
+    const Shares shares = first_item<kThreads, kKeys, kLead, kWindow>(p, kR, c, s_pre, s_sums, s_first, it);
     const int u_begin = c < shares.C ? shares.begin(c) : 0, u_end = c < shares.C ? shares.begin(c + 1) : 0;
     // the stages of an item in this CTA's share: [st0, st1)
     auto stages_of = [&](const Item &x, int &st0, int &st1) {
@@ -372,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
     // the next item with stages in the share; false: there is none
     auto go_on = [&]() {
         if (it.first + it.span >= u_end) return false;
-        next_item<kKeys, kLead>(p, kR, it);
+        next_item<kKeys, kLead, kWindow>(p, kR, it);
         return stages_of(it, st0, st1);
     };
     if (warp == kWMma) {
@@ -398,7 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
             const bool mine = wg * kTileRows < rows;   // (the whole warpgroup) this tile has rows
             // ---- the row's query
             float c_row = 0.f, l0 = 0.f, l1 = 0.f;
-            int lim = 0;
+            int lim = 0, low = 0;
+            const Gap gap = kWindow ? tile_gap<kKeys>(p, it.s, kR, it.qt) : Gap{0, 0};
+            auto first_key = [&](int st) { return (kWindow ? gap.key_unit(st) : st) * kKeys; };
             {
                 // whole rows at a time into the warp's part of the tile, then each thread its own
                 constexpr int kPieces = D / 8, kAtOnce = 32 / kPieces;
@@ -426,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                 float f = pow2_biased(262 - e);   // the largest to [2^8, 2^9)
                 if (p.scale < 0.f) f = -f;   // so that the largest product is the largest score
                 if (there) lim = it.s.len - it.s.nq + qi + 1;
+                if (kWindow && there) low = window_low(p, lim - 1);
                 c_row = fabsf(p.scale) * kLog2e * pow2_biased(e - 8);
                 if (big >= 0x7F80u && lim > 0) l0 = __uint_as_float(0x7fc00000u);   // a query that is not finite: NaN, where it sees a key
                 uint8_t *const tile = sQ + wg * Cfg::kTile;
@@ -447,6 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                 if (lane == 0) mbar_arrive(&bars.q_full);
             }
             const int least = __reduce_min_sync(0xffffffffu, lim);
+            const int low_last = kWindow ? __reduce_max_sync(0xffffffffu, low) : 0;
             float m = kNoMax;   // the exponent taken off: that of the largest probability (or product), less 7 to 15
             int F = 1;
             int st = st0;
@@ -464,11 +475,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                 for (int i = 0; i < 4; ++i) wait_ld(*reinterpret_cast<float(*)[32]>(x + i * 32));
                 const float ct = fmaxf(c_row * pow2_biased(E), 1e-37f);
                 float mx[4];
-                if (st * kKeys + kKeys > least) {
-                    const int left = lim - st * kKeys;   // keys of the stage that the row sees
+                const int key0 = first_key(st);
+                if (key0 + kKeys > least) {
+                    const int left = lim - key0;   // keys of the stage that the row sees
 #pragma unroll
                     for (int j = 0; j < 128; ++j)
                         if (j >= left) x[j] = -INFINITY;
+                }
+                if (kWindow && key0 < low_last && key0 + kKeys > p.sinks) {
+                    const int before = low - key0, sinks = p.sinks - key0;   // keys [sinks, before) are hidden
+#pragma unroll
+                    for (int j = 0; j < 128; ++j)
+                        if (j < before && j >= sinks) x[j] = -INFINITY;
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) mx[i] = x[i];
@@ -518,7 +536,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                 }
                 const int Fn = s_F[g & 3];
                 float state[3] = {m, l0, l1};
-                codes_stage<D>(state, tS, tO, CodesStage{s_scale[g % 3], c_row, lim - st * kKeys, Fn - F, st > st0, codes});
+                codes_stage<D, kWindow>(state, tS, tO, CodesStage{s_scale[g % 3], c_row, lim - first_key(st), Fn - F, st > st0, codes,
+                                                                  low - first_key(st), p.sinks - first_key(st)});
                 m = state[0];
                 l0 = state[1];
                 l1 = state[2];
@@ -621,13 +640,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
         for (;;) {
             const int len = it.s.len;
             const int32_t *table = p.b.table + (size_t)it.b * p.b.max_pages;
+            const Gap gap = kWindow ? tile_gap<kKeys>(p, it.s, kR, it.qt) : Gap{0, 0};
+            const int low = kWindow ? window_low(p, len - it.s.nq + it.qt * kR / p.G) : 0;   // of the item's first row
+            auto first_key = [&](int st) { return (kWindow ? gap.key_unit(st) : st) * kKeys; };
+            // (a run that no row sees is not read: its page may be gone)
+            auto in_reach = [&](int key) { return key < len && (!kWindow || key < p.sinks || key > low - 16); };
             auto page_of = [&](int st) {
-                const int key = st * kKeys + run;
-                return st < st1 && key < len ? ld_here(table + (key >> p.b.shift)) : -1;
+                const int key = first_key(st) + run;
+                return st < st1 && in_reach(key) ? ld_here(table + (key >> p.b.shift)) : -1;
             };
             auto place = [&](int st, int page) {   // the run's first row (row indexes are below 2^32 - 1)
-                const int key = st * kKeys + run;
-                if (st >= st1 || key >= len) return kNone;
+                const int key = first_key(st) + run;
+                if (st >= st1 || !in_reach(key)) return kNone;
                 if ((unsigned)page >= (unsigned)p.c.n_pages) {
                     set_error(p.ctrl, MOE_ERR_DEVICE);
                     return kNone;
@@ -660,7 +684,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                 uint4 w[Cfg::kChunks];
 #pragma unroll
                 for (int i = 0; i < Cfg::kChunks; ++i) w[i] = lds_v4(raw + (lane * Cfg::kChunks + (i ^ turned(lane))) * 16);
-                const bool there = at0 != kNone && st * kKeys + r < len;
+                const int key = first_key(st) + r;
+                const bool there = at0 != kNone && key < len;
                 const uint16_t ks = there ? scales[slot][0][lane] : (uint16_t)0, vs = there ? scales[slot][1][lane] : (uint16_t)0;
                 __syncwarp();
                 slot = slot == 2 ? 0 : slot + 1;
@@ -675,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                 const bool bad = !finite_bits(ks) || !finite_bits(vs);
                 const float kf = bad ? 0.f : bf16_bits_to_f32(ks), vf = bad ? 0.f : bf16_bits_to_f32(vs);
                 // (a row of zeros in V lies far below the others: its key may have all the probability)
-                const int ke = exponent_of(kf, kNoExponent), ve = exponent_of(vf, st * kKeys + r < len && !bad ? -100 : kNoExponent);
+                const int ke = exponent_of(kf, kNoExponent), ve = exponent_of(vf, in_reach(key & ~15) && key < len && !bad ? -100 : kNoExponent);
                 // (most stages change nothing: that is seen at the barrier alone. With four reductions a warp
                 // for each stage's own exponents the prompt chunk took 756 us, so 732; with the first stage's
                 // before the wait 850)
@@ -819,9 +844,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
     if (warp == kWMma) tc::dealloc(tmem, 512);
 }
 
-template <int D>
+template <int D, bool kWindow>
 cudaError_t launch_one(const Attn &p, int *grid_out, cudaStream_t s) {
-    const void *fn = reinterpret_cast<const void *>(kv4_prompt_kernel<D>);
+    const void *fn = reinterpret_cast<const void *>(kv4_prompt_kernel<D, kWindow>);
     // The register split takes what the launch reserves: it must be the whole of it.
     static const bool split_ok = [fn] {
         cudaFuncAttributes a;
@@ -834,13 +859,14 @@ cudaError_t launch_one(const Attn &p, int *grid_out, cudaStream_t s) {
     int grid = sm_count();
     if (grid > kMaxPromptCtas) grid = kMaxPromptCtas;
     *grid_out = grid;
-    return launch_pdl(kv4_prompt_kernel<D>, dim3((unsigned)grid), kThreads, kBase, s, p);
+    return launch_pdl(kv4_prompt_kernel<D, kWindow>, dim3((unsigned)grid), kThreads, kBase, s, p);
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_prompt(const kv4::Attn &p, int *grid, cudaStream_t s) {
-    return p.c.D == 64 ? launch_one<64>(p, grid, s) : launch_one<128>(p, grid, s);
+    if (p.window) return p.c.D == 64 ? launch_one<64, true>(p, grid, s) : launch_one<128, true>(p, grid, s);
+    return p.c.D == 64 ? launch_one<64, false>(p, grid, s) : launch_one<128, false>(p, grid, s);
 }
 
 }  // namespace moe
