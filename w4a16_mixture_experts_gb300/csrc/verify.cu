@@ -15,8 +15,14 @@
 // launches: rows' statistics by chunks, over all rows at once (which row decides is
 // known only after them), then the decision and the race, by chunks of the
 // deciding row; the last CTA of a sequence to finish joins its chunks.
+//
+// The race is run in fp32, with bounds on each score (kSlack below). Where the
+// bounds leave more than one token, those are weighed again in 64 bits, as is a
+// draft whose test they leave open: 64-bit exponentials for all tokens of the row
+// took 1429 us (32 sequences of 4 drafts, 248320 tokens).
 #include <math.h>
 
+#include "kv4_kernels.cuh"
 #include "step_kernels.cuh"
 
 namespace moe {
@@ -27,16 +33,20 @@ constexpr int kThreads = 256, kVecs = 4;            // 16-byte loads of a thread
 constexpr int kChunk = kThreads * 8 * kVecs;        // logits of a chunk
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinNoise = 1.17549435e-38f;
+// How far an fp32 probability may be off, relative: its exponent, up to 127 in size
+// where it is not zero, by two roundings and that of the rate (3 x 127 x 2^-25, times
+// log 2), the exponential and the reciprocals by 2^-22 each, the row's sum by less.
+constexpr float kSlack = 1.f / 65536.f;
+constexpr float kSlackAbs = 2.4e-38f;   // and what fp32 holds as zero
 
 struct Stat {       // of a chunk of a row
-    float m, s;     // the largest logit, the sum of exp((l - m) / t)
-    int arg;        // the first place of m
-    int bad;        // a NaN or +inf among them
+    float m, s;     // the largest logit, the sum of exp((l - m) / t): NaN where a logit is NaN or +inf
+    int arg, pad;   // (t = 0) the first place of m
 };
 
-struct Best {
-    double score;
-    int v, pad;
+struct Best {           // of a chunk: the token ahead, and bounds on its score
+    double low, high;
+    int v, pad;         // v < 0: none has a weight
 };
 
 struct Params {
@@ -108,9 +118,25 @@ __device__ inline void unpack8(const uint4 &v, float (&x)[8]) {
     }
 }
 
+__device__ inline float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ inline float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// s * exp2((m - top) * rate), also where both are -inf and s is 0 (or NaN, which stays).
+__device__ inline float lowered(float s, float m, float top, float rate) { return m == top ? s : s * ex2((m - top) * rate); }
+
 __global__ void __launch_bounds__(kThreads) verify_stats_kernel(const __grid_constant__ Params p) {
     __shared__ float s_m[kThreads / 32], s_s[kThreads / 32];
-    __shared__ int s_arg[kThreads / 32], s_bad[kThreads / 32];
+    __shared__ int s_arg;
+    pdl_wait();
+    pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.x == 0)
         for (int b = threadIdx.x; b < p.B; b += kThreads) p.tickets[b] = 0;
@@ -121,256 +147,369 @@ __global__ void __launch_bounds__(kThreads) verify_stats_kernel(const __grid_con
     if (b < 0) return;
     const float t = p.temperature ? p.temperature[b] : 1.f;
     if (side && (t == 0.f || r + 1 >= p.cu[b + 1])) return;   // not looked at
-    const float rate = t == 0.f ? 0.f : rate_of(t);
+    const float rate = t == 0.f ? 1.f : rate_of(t);
     const uint16_t *row = side ? p.draft + r * p.ds : p.logits + r * p.ls;
     uint4 v[kVecs];
     const int v0 = c * kChunk + threadIdx.x * 8;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) v[i] = load8(row, v0 + i * kThreads * 8, p.V);
-    float m = -INFINITY;
-    int arg = 0x7fffffff, bad = 0;
+    __nv_bfloat162 m2 = __floats2bfloat162_rn(-INFINITY, -INFINITY);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-        float x[8];
-        unpack8(v[i], x);
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            bad |= !(x[j] < INFINITY);
-            if (x[j] > m) {
-                m = x[j];
-                arg = v0 + i * kThreads * 8 + j;
-            }
-        }
+        for (int j = 0; j < 4; ++j) m2 = __hmax2(m2, *reinterpret_cast<const __nv_bfloat162 *>(&w[j]));
     }
-    float top = m;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float om = __shfl_xor_sync(0xffffffffu, top, o);
-        const int oa = __shfl_xor_sync(0xffffffffu, arg, o);
-        if (om > top || (om == top && oa < arg)) arg = oa;
-        top = fmaxf(top, om);
-    }
+    const float mine = fmaxf(__low2float(m2), __high2float(m2)), top = warp_max(mine);
+    // The sum is taken against the whole number of octaves nearest to the largest (one rounding a
+    // term), and brought to the largest itself at the end; where that number is not small, term by term.
     float s = 0.f;
-    if (top > -INFINITY && rate > 0.f) {
+    const float octaves = rintf(top * rate);
+    if (fabsf(octaves) < 65536.f) {
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
             float x[8];
             unpack8(v[i], x);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s += ex2((x[j] - top) * rate);
+            for (int j = 0; j < 8; ++j) s += ex2(fmaf(x[j], rate, -octaves));
+        }
+        s *= ex2(fmaf(-top, rate, octaves));
+    } else {
+        const float from = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            float x[8];
+            unpack8(v[i], x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s += ex2((x[j] - from) * rate);
         }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    bad = __any_sync(0xffffffffu, bad);
+    s = warp_sum(s);
     if (lane == 0) {
         s_m[warp] = top;
         s_s[warp] = s;
-        s_arg[warp] = arg;
-        s_bad[warp] = bad;
     }
+    if (threadIdx.x == 0) s_arg = 0x7fffffff;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        Stat st{s_m[0], 0.f, s_arg[0], 0};
-        for (int w = 1; w < kThreads / 32; ++w)
-            if (s_m[w] > st.m || (s_m[w] == st.m && s_arg[w] < st.arg)) {
-                st.m = s_m[w];
-                st.arg = s_arg[w];
+    float all = s_m[0];
+#pragma unroll
+    for (int w = 1; w < kThreads / 32; ++w) all = fmaxf(all, s_m[w]);
+    if (t == 0.f) {
+        if (mine == all) {
+            int first = 0x7fffffff;
+#pragma unroll
+            for (int i = kVecs - 1; i >= 0; --i) {
+                float x[8];
+                unpack8(v[i], x);
+#pragma unroll
+                for (int j = 7; j >= 0; --j)
+                    if (x[j] == all) first = v0 + i * kThreads * 8 + j;
             }
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (s_s[w] > 0.f) st.s += s_s[w] * ex2((s_m[w] - st.m) * rate);
-            st.bad |= s_bad[w];
+            atomicMin(&s_arg, first);
         }
-        p.stats[((size_t)r * sides + side) * p.chunks + c] = st;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        float sum = 0.f;
+        for (int w = 0; w < kThreads / 32; ++w) sum += lowered(s_s[w], s_m[w], all, rate);
+        p.stats[((size_t)r * sides + side) * p.chunks + c] = Stat{all, sum, s_arg, 0};
     }
 }
 
 struct Row {
-    float m;     // the largest logit
-    double z;    // the sum of exp((l - m) / t)
-    int arg, bad;
+    float m, z;     // the largest logit, the sum of exp((l - m) / t)
+    int arg;        // (t = 0) the first place of m
+    bool bad;       // no distribution: a NaN, a +inf, nothing but -inf
 };
 
+// A whole warp calls it, a chunk a lane.
 __device__ inline Row row_stats(const Params &p, int r, int side, float rate) {
     const Stat *st = p.stats + ((size_t)r * (p.draft ? 2 : 1) + side) * p.chunks;
-    Row o{-INFINITY, 0.0, 0, 0};
-    for (int c = 0; c < p.chunks; ++c) {
-        const Stat s = st[c];
-        o.bad |= s.bad;
-        if (s.m > o.m) {
-            o.m = s.m;
-            o.arg = s.arg;
-        }
+    const int lane = threadIdx.x & 31;
+    Row o{-INFINITY, 0.f, 0x7fffffff, false};
+    for (int c0 = 0; c0 < p.chunks; c0 += 32) {
+        const bool in = c0 + lane < p.chunks;
+        const Stat s = in ? st[c0 + lane] : Stat{-INFINITY, 0.f, 0x7fffffff, 0};
+        const float m = fmaxf(o.m, warp_max(s.m));
+        const int arg = __reduce_min_sync(0xffffffffu, s.m == m ? s.arg : 0x7fffffff);
+        o.arg = m > o.m ? arg : min(o.arg, arg);
+        o.z = lowered(o.z, o.m, m, rate) + warp_sum(lowered(s.s, s.m, m, rate));
+        o.m = m;
     }
-    for (int c = 0; c < p.chunks; ++c)
-        if (st[c].s > 0.f) o.z += (double)st[c].s * exp2((double)((st[c].m - o.m) * rate));
-    o.bad |= !(o.m > -INFINITY);
+    o.bad = !(o.m > -INFINITY && o.z < INFINITY);
     return o;
 }
 
-__device__ inline double probability(const Row &o, float l, float t) { return exp(((double)l - (double)o.m) / (double)t) / o.z; }
-
 struct Decision {
-    int r0, n, a, state;   // rows of the sequence, accepted drafts; 0: the race decides, 1: `chosen` does
-    int chosen, last, x;   // the draft that was refused (its q is 1 without draft logits; -1: none)
-    float t, rate, mp, mq;
-    double zp, zq;
+    int r0, n, a;       // rows of the sequence, accepted drafts
+    int chosen;         // the next token where the race does not decide (state 1)
+    int state, last;    // the deciding row is the last
+    int x;              // the draft that it refused: its q is 1 without draft logits (< 0: none)
+    float t, rate, mp, mq, zp, zq;
 };
 
-// What becomes of sequence b: a whole warp calls it, a draft a lane.
+// In 64 bits: is u * q(x) < p(x)?
+__device__ __noinline__ bool accepts(float u, float l, float mp, float zp, bool has_q, float ld, float mq, float zq, float t) {
+    const double pv = exp(((double)l - mp) / t) / zp, qv = has_q ? exp(((double)ld - mq) / t) / zq : 1.0;
+    return (double)u * qv < pv;
+}
+
+struct Test {   // of a row's draft
+    Row p, q;
+    int x, stop, fault, last;
+};
+
+// What becomes of sequence b: all threads call it, a row a warp.
 __device__ inline Decision decide(const Params &p, int b) {
-    const int lane = threadIdx.x & 31;
+    __shared__ Test s_test[kThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Rows rows = rows_of(p, b);
-    Decision d;
-    d.r0 = rows.r0;
-    d.n = rows.n;
-    d.t = p.temperature ? p.temperature[b] : 1.f;
-    d.a = 0;
-    d.state = 1;
-    d.chosen = -1;
-    d.last = 0;
-    d.x = -1;
-    d.mp = d.mq = 0.f;
-    d.zp = d.zq = 1.0;
-    const bool greedy = d.t == 0.f, bad_t = !(d.t >= 0.f && d.t < INFINITY);
-    d.rate = greedy ? 0.f : rate_of(d.t);
-    if (bad_t && rows.n > 0) set_error(p.ctrl, MOE_ERR_DEVICE);
-    if (rows.n == 0 || bad_t) return d;
-    for (int i0 = 0;; i0 += 32) {
-        const int i = i0 + lane, r = rows.r0 + i;
-        const bool there = i < rows.n, last = i == rows.n - 1;
-        Row tp{0.f, 1.0, 0, 0}, tq{0.f, 1.0, 0, 0};
-        bool stop = !there, fault = false;
-        int x = -1;
-        if (there) {
-            tp = row_stats(p, r, 0, d.rate);
-            fault = tp.bad;
-            stop = last || fault;
-            if (!stop) {
-                x = p.drafts[r];
-                const bool known = (unsigned)x < (unsigned)p.V;
+    Decision d{rows.r0, rows.n, 0, -1, 1, 0, -1, p.temperature ? p.temperature[b] : 1.f, 0.f, 0.f, 0.f, 1.f, 1.f};
+    const bool greedy = d.t == 0.f;
+    if (!(d.t >= 0.f && d.t < INFINITY)) {
+        if (rows.n > 0) set_error(p.ctrl, MOE_ERR_DEVICE);
+        return d;
+    }
+    if (rows.n == 0) return d;
+    d.rate = greedy ? 1.f : rate_of(d.t);
+    for (int i0 = 0;; i0 += kThreads / 32) {
+        const int i = i0 + warp, r = rows.r0 + i;
+        Test t{{0.f, 1.f, 0, false}, {0.f, 1.f, 0, false}, -1, 1, 0, 0};
+        if (i < rows.n) {
+            t.last = i == rows.n - 1;
+            const bool has_q = p.draft && !greedy && !t.last;
+            const int x = t.last ? -1 : p.drafts[r];
+            const bool known = (unsigned)x < (unsigned)p.V;
+            const float l = known ? bf16_bits_to_f32(p.logits[r * p.ls + x]) : 0.f;
+            const float ld = known && has_q ? bf16_bits_to_f32(p.draft[r * p.ds + x]) : 0.f;
+            const float u = t.last ? 0.f : p.uniform[r];
+            t.p = row_stats(p, r, 0, d.rate);
+            if (has_q) t.q = row_stats(p, r, 1, d.rate);
+            t.x = t.last ? -1 : known ? x : -2;
+            t.fault = t.p.bad || t.q.bad;
+            if (!t.last && !t.fault && known) {
                 if (greedy) {
-                    stop = tp.arg != x;
+                    t.stop = t.p.arg != x;
                 } else {
-                    double q = 1.0;
-                    if (p.draft) {
-                        tq = row_stats(p, r, 1, d.rate);
-                        fault = tq.bad;
-                        if (known) q = probability(tq, bf16_bits_to_f32(p.draft[r * p.ds + x]), d.t);
-                    }
-                    stop = fault || !known || !((double)p.uniform[r] * q < probability(tp, bf16_bits_to_f32(p.logits[r * p.ls + x]), d.t));
+                    const float pv = ex2((l - t.p.m) * d.rate) / t.p.z, uq = has_q ? u * (ex2((ld - t.q.m) * d.rate) / t.q.z) : u;
+                    if (fabsf(pv - uq) > 2.f * kSlack * (pv + fabsf(uq)) && fmaxf(pv, fabsf(uq)) > 1e-30f) t.stop = !(uq < pv);
+                    else t.stop = !accepts(u, l, t.p.m, t.p.z, has_q, ld, t.q.m, t.q.z, d.t);
                 }
-                if (!known) x = -2;
             }
         }
-        const uint32_t m = __ballot_sync(0xffffffffu, stop);
-        // an unknown token that is reached is an error too
-        if (m) {
-            const int k = __ffs(m) - 1;
-            d.a = i0 + k;
-            d.last = __shfl_sync(0xffffffffu, (int)last, k);
-            d.x = __shfl_sync(0xffffffffu, x, k);
-            d.mp = __shfl_sync(0xffffffffu, tp.m, k);
-            d.mq = __shfl_sync(0xffffffffu, tq.m, k);
-            d.zp = __shfl_sync(0xffffffffu, tp.z, k);
-            d.zq = __shfl_sync(0xffffffffu, tq.z, k);
-            const bool f = __shfl_sync(0xffffffffu, (int)fault, k);
-            if (f || d.x == -2) set_error(p.ctrl, MOE_ERR_DEVICE);
-            d.state = f || greedy;
-            d.chosen = f ? -1 : __shfl_sync(0xffffffffu, tp.arg, k);
-            return d;
-        }
+        if (i0) __syncthreads();
+        if (lane == 0) s_test[warp] = t;
+        __syncthreads();
+        int k = 0;
+        while (k < kThreads / 32 && !s_test[k].stop) ++k;
+        if (k == kThreads / 32) continue;
+        const Test &e = s_test[k];
+        d.a = i0 + k;
+        d.last = e.last;
+        d.x = e.x;
+        d.mp = e.p.m;
+        d.zp = e.p.z;
+        d.mq = e.q.m;
+        d.zq = e.q.z;
+        if ((e.fault || e.x == -2) && threadIdx.x == 0) set_error(p.ctrl, MOE_ERR_DEVICE);
+        d.state = e.fault || greedy;
+        d.chosen = e.fault ? -1 : e.p.arg;
+        return d;
     }
 }
 
-// Weight of token v with logits l and ld, in 64 bits.
-__device__ inline double weight(const Params &p, const Decision &d, int v, float l, float ld, bool residual) {
-    const double pv = exp(((double)l - (double)d.mp) / (double)d.t) / d.zp;
-    if (!residual) return pv;
-    if (!p.draft) return v == d.x ? 0.0 : pv;
-    return fmax(pv - exp(((double)ld - (double)d.mq) / (double)d.t) / d.zq, 0.0);
-}
+// The deciding row's values and what a token weighs in it.
+struct Weigh {
+    const Params &p;
+    const Decision &d;
+    const uint16_t *row, *drow;   // drow: where q is taken off
+    const float *noise;
+    int none;                     // a token without weight
 
-__device__ inline float noise_of(float e) { return e >= kMinNoise ? e : kMinNoise; }
+    __device__ Weigh(const Params &p_, const Decision &d_, int b, bool residual)
+        : p(p_), d(d_), row(p_.logits + (d_.r0 + d_.a) * p_.ls), drow(residual && p_.draft ? p_.draft + (d_.r0 + d_.a) * p_.ds : nullptr),
+          noise(p_.noise + b * p_.ns), none(residual && !p_.draft ? d_.x : -1) {}
 
-// The race over the tokens of chunk c of the deciding row.
-__device__ Best race(const Params &p, const Decision &d, int c, bool residual) {
+    __device__ static float noise_of(float e) { return e >= kMinNoise ? e : kMinNoise; }
+
+    // in 64 bits; negative: no weight
+    __device__ __noinline__ double score(int v) const {
+        if (v == none) return -1.0;
+        double w = exp(((double)bf16_bits_to_f32(row[v]) - d.mp) / d.t) / d.zp;
+        if (drow) w -= exp(((double)bf16_bits_to_f32(drow[v]) - d.mq) / d.t) / d.zq;
+        return w > 0.0 ? w / (double)noise_of(noise[v]) : -1.0;
+    }
+};
+
+// (score, v) of the token that is ahead of all of the block's: all threads call it.
+__device__ inline void ahead(double &score, int &v) {
     __shared__ double s_score[kThreads / 32];
     __shared__ int s_v[kThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint16_t *row = p.logits + (d.r0 + d.a) * p.ls, *drow = p.draft ? p.draft + (d.r0 + d.a) * p.ds : nullptr;
-    const float *noise = p.noise + blockIdx.y * p.ns;
-    double score = 0.0;
-    int best = -1;
-    for (int i = 0; i < kVecs * 8; ++i) {
-        const int v = c * kChunk + i * kThreads + threadIdx.x;
-        if (v >= p.V) break;
-        const double w = weight(p, d, v, bf16_bits_to_f32(row[v]), drow && residual ? bf16_bits_to_f32(drow[v]) : 0.f, residual);
-        const double s = w / (double)noise_of(noise[v]);
-        if (w > 0.0 && (best < 0 || s > score)) {
-            score = s;
-            best = v;
-        }
-    }
-    for (int o = 16; o > 0; o >>= 1) {
-        const double os = __shfl_xor_sync(0xffffffffu, score, o);
-        const int ov = __shfl_xor_sync(0xffffffffu, best, o);
-        if (ov >= 0 && (best < 0 || os > score || (os == score && ov < best))) {
+    auto join = [&](double os, int ov) {
+        if (ov >= 0 && (v < 0 || os > score || (os == score && ov < v))) {
             score = os;
-            best = ov;
+            v = ov;
         }
-    }
+    };
+    for (int o = 16; o > 0; o >>= 1) join(__shfl_xor_sync(0xffffffffu, score, o), __shfl_xor_sync(0xffffffffu, v, o));
     __syncthreads();
     if (lane == 0) {
         s_score[warp] = score;
-        s_v[warp] = best;
+        s_v[warp] = v;
     }
     __syncthreads();
-    Best o{s_score[0], s_v[0], 0};
-    for (int w = 1; w < kThreads / 32; ++w)
-        if (s_v[w] >= 0 && (o.v < 0 || s_score[w] > o.score || (s_score[w] == o.score && s_v[w] < o.v))) {
-            o.score = s_score[w];
-            o.v = s_v[w];
+    for (int w = 0; w < kThreads / 32; ++w) join(s_score[w], s_v[w]);
+}
+
+__device__ inline void noise8(const float *noise, int v, int V, float (&e)[8]) {
+    if (v + 8 <= V) {
+        const float4 a = *reinterpret_cast<const float4 *>(noise + v), b = *reinterpret_cast<const float4 *>(noise + v + 4);
+        e[0] = a.x, e[1] = a.y, e[2] = a.z, e[3] = a.w, e[4] = b.x, e[5] = b.y, e[6] = b.z, e[7] = b.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = v + i < V ? noise[v + i] : 1.f;
+    }
+}
+
+// The race over the tokens of chunk c of the deciding row.
+__device__ inline Best race(const Weigh &w, int c) {
+    __shared__ float s_low[kThreads / 32];
+    const Params &p = w.p;
+    const Decision &d = w.d;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, v0 = c * kChunk + threadIdx.x * 8;
+    uint4 lv[kVecs], dv[kVecs];
+    float e[kVecs][8];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+        lv[i] = load8(w.row, v0 + i * kThreads * 8, p.V);
+        dv[i] = w.drow ? load8(w.drow, v0 + i * kThreads * 8, p.V) : make_uint4(0, 0, 0, 0);
+        noise8(w.noise, v0 + i * kThreads * 8, p.V, e[i]);
+    }
+    const float lzp = -log2f(d.zp), lzq = -log2f(d.zq);
+    // bounds on a token's score; high < 0: no weight
+    auto bounds = [&](float l, float ld, float noise, int v, float &low, float &high) {
+        const float pv = ex2(fmaf(l - d.mp, d.rate, lzp)), qv = w.drow ? ex2(fmaf(ld - d.mq, d.rate, lzq)) : 0.f;
+        const float r = pv - qv, off = fmaf(kSlack, pv + qv, kSlackAbs), inv = __fdividef(1.f, Weigh::noise_of(noise));
+        low = (r - off) * inv;
+        high = r + off > 0.f && v != w.none && l > -INFINITY ? (r + off) * inv : -1.f;
+        if (v == w.none) low = 0.f;
+    };
+    float low = 0.f, high = -1.f;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+        float x[8], y[8];
+        unpack8(lv[i], x);
+        unpack8(dv[i], y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float lo, hi;
+            bounds(x[j], y[j], e[i][j], v0 + i * kThreads * 8 + j, lo, hi);
+            low = fmaxf(low, lo);
+            high = fmaxf(high, hi);
         }
-    return o;
+    }
+    low = warp_max(low);
+    __syncthreads();
+    if (lane == 0) s_low[warp] = low;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kThreads / 32; ++k) low = fmaxf(low, s_low[k]);
+    // who may be ahead of all
+    int count = 0;
+    Best o{0.0, 0.0, -1, 0};
+    if (high >= low) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            float x[8], y[8];
+            unpack8(lv[i], x);
+            unpack8(dv[i], y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float lo, hi;
+                bounds(x[j], y[j], e[i][j], v0 + i * kThreads * 8 + j, lo, hi);
+                if (hi >= low) {
+                    ++count;
+                    o = Best{fmaxf(lo, 0.f), hi, v0 + i * kThreads * 8 + j, 0};
+                }
+            }
+        }
+    }
+    const int some = __syncthreads_count(count > 0), many = __syncthreads_or(count > 1);
+    if (some == 0) return Best{0.0, 0.0, -1, 0};
+    if (some == 1 && !many && low > 0.f) {   // one, and it has a weight
+        if (count == 1) p.best[blockIdx.y * (size_t)p.chunks + c] = o;
+        o.v = -2;   // (written)
+        return o;
+    }
+    double score = 0.0;
+    int v = -1;
+    if (count > 0)
+        for (int i = 0; i < kVecs; ++i)
+            for (int j = 0; j < 8; ++j) {
+                const int k = v0 + i * kThreads * 8 + j;
+                if (k >= p.V) break;
+                float lo, hi;
+                bounds(bf16_bits_to_f32(w.row[k]), w.drow ? bf16_bits_to_f32(w.drow[k]) : 0.f, w.noise[k], k, lo, hi);
+                if (hi < low) continue;
+                const double s = w.score(k);
+                if (s >= 0.0 && (v < 0 || s > score)) {
+                    score = s;
+                    v = k;
+                }
+            }
+    ahead(score, v);
+    return Best{score, score, v, 0};
 }
 
 __global__ void __launch_bounds__(kThreads) verify_choose_kernel(const __grid_constant__ Params p) {
-    __shared__ Decision s_d;
     __shared__ bool s_last;
+    pdl_wait();
+    pdl_launch_dependents();
     const int b = blockIdx.y, c = blockIdx.x;
-    if (threadIdx.x < 32) {
-        const Decision d = decide(p, b);
-        if (threadIdx.x == 0) s_d = d;
-    }
-    __syncthreads();
-    const Decision d = s_d;
-    const bool residual = !d.last;
-    if (d.state == 0) {
-        const Best o = race(p, d, c, residual);
-        if (threadIdx.x == 0) p.best[(size_t)b * p.chunks + c] = o;
-    }
-    if (threadIdx.x == 0) {
-        __threadfence();
-        s_last = atom_acq_rel_add_u32(p.tickets + b, 1) == (uint32_t)p.chunks - 1;
-    }
-    __syncthreads();
-    if (!s_last) return;
+    const Decision d = decide(p, b);
     int chosen = d.chosen;
     if (d.state == 0) {
-        Best o{0.0, -1, 0};
-        for (int k = 0; k < p.chunks; ++k) {   // (in order of the tokens: ties stay with the first)
-            const Best *q = p.best + (size_t)b * p.chunks + k;
-            const double s = __ldcg(&q->score);
-            const int v = __ldcg(&q->v);
-            if (v >= 0 && (o.v < 0 || s > o.score)) o = Best{s, v, 0};
+        const bool residual = !d.last;
+        const Best o = race(Weigh(p, d, b, residual), c);
+        if (o.v != -2 && threadIdx.x == 0) p.best[(size_t)b * p.chunks + c] = o;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            __threadfence();
+            s_last = atom_acq_rel_add_u32(p.tickets + b, 1) == (uint32_t)p.chunks - 1;
+            __threadfence();
         }
-        if (o.v < 0)   // nothing is left of p - q: p itself
+        __syncthreads();
+        if (!s_last) return;
+        // ---- the chunks' first ones against one another
+        double low = 0.0, score = 0.0;
+        int v = -1;
+        const Best *best = p.best + (size_t)b * p.chunks;
+        for (int k = 0; k < p.chunks; ++k) low = fmax(low, __ldcg(&best[k].low));
+        const Best mine = threadIdx.x < p.chunks ? Best{0.0, __ldcg(&best[threadIdx.x].high), __ldcg(&best[threadIdx.x].v), 0} : Best{0.0, 0.0, -1, 0};
+        const bool in = mine.v >= 0 && mine.high >= low;
+        static_assert(kThreads * kChunk >= 1 << 20, "a thread a chunk");
+        const int some = __syncthreads_count(in);
+        if (in) {
+            v = mine.v;
+            score = some > 1 ? Weigh(p, d, b, residual).score(v) : 0.0;
+        }
+        ahead(score, v);
+        if (v < 0)   // nothing is left of p - q: p itself
             for (int k = 0; k < p.chunks; ++k) {
-                const Best x = race(p, d, k, false);
-                if (x.v >= 0 && (o.v < 0 || x.score > o.score)) o = x;
+                const Weigh w(p, d, b, false);
+                for (int i = threadIdx.x; i < kChunk && k * kChunk + i < p.V; i += kThreads) {
+                    const double s = w.score(k * kChunk + i);
+                    if (s >= 0.0 && (v < 0 || s > score || (s == score && k * kChunk + i < v))) {
+                        score = s;
+                        v = k * kChunk + i;
+                    }
+                }
+                if (k == p.chunks - 1) ahead(score, v);
             }
-        chosen = o.v;
+        chosen = v;
+    } else if (c > 0) {
+        return;
     }
     for (int i = threadIdx.x; i < d.n; i += kThreads) p.tokens[d.r0 + i] = i < d.a ? p.drafts[d.r0 + i] : i == d.a ? chosen : -1;
     if (threadIdx.x == 0) p.accepted[b] = d.a;
@@ -398,11 +537,9 @@ cudaError_t launch_verify(const VerifyArgs &a, int B, int T, int V, void *ws, cu
     const Layout L = layout(B, T, V, a.draft != nullptr);
     const Params p{a.logits, a.draft, a.ls, a.ds, a.ns, a.drafts, a.cu, a.temperature, a.uniform, a.noise, a.tokens, a.accepted,
                    B, T, V, L.chunks, reinterpret_cast<Ctrl *>(ws), ws_at<uint32_t>(ws, L.tickets), ws_at<Best>(ws, L.best), ws_at<Stat>(ws, L.stats)};
-    verify_stats_kernel<<<(unsigned)((T > 0 ? T : 1) * (a.draft ? 2 : 1) * L.chunks), kThreads, 0, s>>>(p);
-    const cudaError_t err = cudaGetLastError();
+    const cudaError_t err = launch_pdl(verify_stats_kernel, dim3((unsigned)((T > 0 ? T : 1) * (a.draft ? 2 : 1) * L.chunks)), kThreads, 0, s, p);
     if (err != cudaSuccess) return err;
-    verify_choose_kernel<<<dim3((unsigned)L.chunks, (unsigned)B), kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_pdl(verify_choose_kernel, dim3((unsigned)L.chunks, (unsigned)B), kThreads, 0, s, p);
 }
 
 }  // namespace moe
