@@ -29,8 +29,10 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 256, kVecs = 4;            // 16-byte loads of a thread in a chunk
-constexpr int kChunk = kThreads * 8 * kVecs;        // logits of a chunk
+constexpr int kThreads = 256;
+constexpr int kVecs = 8, kChunk = kThreads * 8 * kVecs;   // 16-byte loads of a thread and logits in a chunk of the statistics
+constexpr int kLapVecs = 4, kLap = kThreads * 8 * kLapVecs;   // ... and of the race
+static_assert(kThreads * kLap >= 1 << 20, "a thread a lap");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinNoise = 1.17549435e-38f;
 // How far an fp32 probability may be off, relative: its exponent, up to 127 in size
@@ -44,7 +46,7 @@ struct Stat {       // of a chunk of a row
     int arg, pad;   // (t = 0) the first place of m
 };
 
-struct Best {           // of a chunk: the token ahead, and bounds on its score
+struct Best {           // of a lap: the token ahead, and bounds on its score
     double low, high;
     int v, pad;         // v < 0: none has a weight
 };
@@ -55,10 +57,10 @@ struct Params {
     const int32_t *drafts, *cu;
     const float *temperature, *uniform, *noise;
     int32_t *tokens, *accepted;
-    int B, T, V, chunks;
+    int B, T, V, chunks, laps;
     Ctrl *ctrl;
     uint32_t *tickets;   // [B], cleared by the first launch
-    Best *best;          // [B][chunks]
+    Best *best;          // [B][laps]
     Stat *stats;         // [T][1 or 2][chunks]
 };
 
@@ -118,6 +120,18 @@ __device__ inline void unpack8(const uint4 &v, float (&x)[8]) {
     }
 }
 
+// Adds the exponentials of two logits, a sum each.
+__device__ inline void add_exp2(float &a, float &b, uint32_t w, float rate, float from) {
+    asm("{\n\t.reg .b64 x, y, z;\n\t.reg .f32 u, v;\n\t.reg .b32 lo, hi;\n\t"
+        "shl.b32 lo, %2, 16;\n\tand.b32 hi, %2, 0xffff0000;\n\t"
+        "mov.b64 x, {lo, hi};\n\tmov.b64 y, {%3, %3};\n\tmov.b64 z, {%4, %4};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {u, v}, x;\n\t"
+        "ex2.approx.ftz.f32 u, u;\n\tex2.approx.ftz.f32 v, v;\n\t"
+        "mov.b64 x, {u, v};\n\tmov.b64 y, {%0, %1};\n\tadd.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "r"(w), "f"(rate), "f"(from));
+}
+
 __device__ inline float warp_max(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -151,8 +165,13 @@ __global__ void __launch_bounds__(kThreads) verify_stats_kernel(const __grid_con
     const uint16_t *row = side ? p.draft + r * p.ds : p.logits + r * p.ls;
     uint4 v[kVecs];
     const int v0 = c * kChunk + threadIdx.x * 8;
+    if ((c + 1) * kChunk <= p.V) {
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) v[i] = load8(row, v0 + i * kThreads * 8, p.V);
+        for (int i = 0; i < kVecs; ++i) v[i] = *reinterpret_cast<const uint4 *>(row + v0 + i * kThreads * 8);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) v[i] = load8(row, v0 + i * kThreads * 8, p.V);
+    }
     __nv_bfloat162 m2 = __floats2bfloat162_rn(-INFINITY, -INFINITY);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
@@ -166,14 +185,14 @@ __global__ void __launch_bounds__(kThreads) verify_stats_kernel(const __grid_con
     float s = 0.f;
     const float octaves = rintf(top * rate);
     if (fabsf(octaves) < 65536.f) {
+        float s2 = 0.f;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
-            float x[8];
-            unpack8(v[i], x);
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s += ex2(fmaf(x[j], rate, -octaves));
+            for (int j = 0; j < 4; ++j) add_exp2(s, s2, w[j], rate, -octaves);
         }
-        s *= ex2(fmaf(-top, rate, octaves));
+        s = (s + s2) * ex2(fmaf(-top, rate, octaves));
     } else {
         const float from = top == -INFINITY ? 0.f : top;
 #pragma unroll
@@ -372,20 +391,12 @@ __device__ inline void noise8(const float *noise, int v, int V, float (&e)[8]) {
     }
 }
 
-// The race over the tokens of chunk c of the deciding row.
+// The race over the tokens of lap c of the deciding row.
 __device__ inline Best race(const Weigh &w, int c) {
     __shared__ float s_low[kThreads / 32];
     const Params &p = w.p;
     const Decision &d = w.d;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, v0 = c * kChunk + threadIdx.x * 8;
-    uint4 lv[kVecs], dv[kVecs];
-    float e[kVecs][8];
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-        lv[i] = load8(w.row, v0 + i * kThreads * 8, p.V);
-        dv[i] = w.drow ? load8(w.drow, v0 + i * kThreads * 8, p.V) : make_uint4(0, 0, 0, 0);
-        noise8(w.noise, v0 + i * kThreads * 8, p.V, e[i]);
-    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, v0 = c * kLap + threadIdx.x * 8;
     const float lzp = -log2f(d.zp), lzq = -log2f(d.zq);
     // bounds on a token's score; high < 0: no weight
     auto bounds = [&](float l, float ld, float noise, int v, float &low, float &high) {
@@ -396,19 +407,27 @@ __device__ inline Best race(const Weigh &w, int c) {
         if (v == w.none) low = 0.f;
     };
     float low = 0.f, high = -1.f;
+    auto pass = [&](auto &&each) {
+#pragma unroll 2
+        for (int i = 0; i < kLapVecs; ++i) {
+            const int at = v0 + i * kThreads * 8;
+            const uint4 l = load8(w.row, at, p.V), ld = w.drow ? load8(w.drow, at, p.V) : make_uint4(0, 0, 0, 0);
+            float x[8], y[8], e[8];
+            noise8(w.noise, at, p.V, e);
+            unpack8(l, x);
+            unpack8(ld, y);
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-        float x[8], y[8];
-        unpack8(lv[i], x);
-        unpack8(dv[i], y);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float lo, hi;
-            bounds(x[j], y[j], e[i][j], v0 + i * kThreads * 8 + j, lo, hi);
-            low = fmaxf(low, lo);
-            high = fmaxf(high, hi);
+            for (int j = 0; j < 8; ++j) {
+                float lo, hi;
+                bounds(x[j], y[j], e[j], at + j, lo, hi);
+                each(at + j, lo, hi);
+            }
         }
-    }
+    };
+    pass([&](int, float lo, float hi) {
+        low = fmaxf(low, lo);
+        high = fmaxf(high, hi);
+    });
     low = warp_max(low);
     __syncthreads();
     if (lane == 0) s_low[warp] = low;
@@ -418,95 +437,81 @@ __device__ inline Best race(const Weigh &w, int c) {
     // who may be ahead of all
     int count = 0;
     Best o{0.0, 0.0, -1, 0};
-    if (high >= low) {
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            float x[8], y[8];
-            unpack8(lv[i], x);
-            unpack8(dv[i], y);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float lo, hi;
-                bounds(x[j], y[j], e[i][j], v0 + i * kThreads * 8 + j, lo, hi);
-                if (hi >= low) {
-                    ++count;
-                    o = Best{fmaxf(lo, 0.f), hi, v0 + i * kThreads * 8 + j, 0};
-                }
-            }
-        }
-    }
+    if (high >= low)
+        pass([&](int v, float lo, float hi) {
+            if (hi < low) return;
+            ++count;
+            o = Best{fmaxf(lo, 0.f), hi, v, 0};
+        });
     const int some = __syncthreads_count(count > 0), many = __syncthreads_or(count > 1);
     if (some == 0) return Best{0.0, 0.0, -1, 0};
     if (some == 1 && !many && low > 0.f) {   // one, and it has a weight
-        if (count == 1) p.best[blockIdx.y * (size_t)p.chunks + c] = o;
+        if (count == 1) p.best[blockIdx.y * (size_t)p.laps + c] = o;
         o.v = -2;   // (written)
         return o;
     }
     double score = 0.0;
     int v = -1;
     if (count > 0)
-        for (int i = 0; i < kVecs; ++i)
-            for (int j = 0; j < 8; ++j) {
-                const int k = v0 + i * kThreads * 8 + j;
-                if (k >= p.V) break;
-                float lo, hi;
-                bounds(bf16_bits_to_f32(w.row[k]), w.drow ? bf16_bits_to_f32(w.drow[k]) : 0.f, w.noise[k], k, lo, hi);
-                if (hi < low) continue;
-                const double s = w.score(k);
-                if (s >= 0.0 && (v < 0 || s > score)) {
-                    score = s;
-                    v = k;
-                }
+        pass([&](int k, float, float hi) {
+            if (hi < low) return;
+            const double s = w.score(k);
+            if (s >= 0.0 && (v < 0 || s > score)) {
+                score = s;
+                v = k;
             }
+        });
     ahead(score, v);
     return Best{score, score, v, 0};
 }
 
-__global__ void __launch_bounds__(kThreads) verify_choose_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 3) verify_choose_kernel(const __grid_constant__ Params p) {
     __shared__ bool s_last;
+    const int b = blockIdx.y, c = blockIdx.x;
+    {   // (the noise on its way while the decision is made)
+        const int v = c * kLap + threadIdx.x * 32;
+        if (v < p.V) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.noise + b * p.ns + v));
+    }
     pdl_wait();
     pdl_launch_dependents();
-    const int b = blockIdx.y, c = blockIdx.x;
     const Decision d = decide(p, b);
     int chosen = d.chosen;
     if (d.state == 0) {
         const bool residual = !d.last;
         const Best o = race(Weigh(p, d, b, residual), c);
-        if (o.v != -2 && threadIdx.x == 0) p.best[(size_t)b * p.chunks + c] = o;
+        if (o.v != -2 && threadIdx.x == 0) p.best[(size_t)b * p.laps + c] = o;
         __syncthreads();
         if (threadIdx.x == 0) {
             __threadfence();
-            s_last = atom_acq_rel_add_u32(p.tickets + b, 1) == (uint32_t)p.chunks - 1;
+            s_last = atom_acq_rel_add_u32(p.tickets + b, 1) == (uint32_t)p.laps - 1;
             __threadfence();
         }
         __syncthreads();
         if (!s_last) return;
-        // ---- the chunks' first ones against one another
+        // ---- the laps' first ones against one another
         double low = 0.0, score = 0.0;
         int v = -1;
-        const Best *best = p.best + (size_t)b * p.chunks;
-        for (int k = 0; k < p.chunks; ++k) low = fmax(low, __ldcg(&best[k].low));
-        const Best mine = threadIdx.x < p.chunks ? Best{0.0, __ldcg(&best[threadIdx.x].high), __ldcg(&best[threadIdx.x].v), 0} : Best{0.0, 0.0, -1, 0};
+        const Best *best = p.best + (size_t)b * p.laps;
+        for (int k = 0; k < p.laps; ++k) low = fmax(low, __ldcg(&best[k].low));
+        const Best mine = threadIdx.x < p.laps ? Best{0.0, __ldcg(&best[threadIdx.x].high), __ldcg(&best[threadIdx.x].v), 0} : Best{0.0, 0.0, -1, 0};
         const bool in = mine.v >= 0 && mine.high >= low;
-        static_assert(kThreads * kChunk >= 1 << 20, "a thread a chunk");
         const int some = __syncthreads_count(in);
         if (in) {
             v = mine.v;
             score = some > 1 ? Weigh(p, d, b, residual).score(v) : 0.0;
         }
         ahead(score, v);
-        if (v < 0)   // nothing is left of p - q: p itself
-            for (int k = 0; k < p.chunks; ++k) {
-                const Weigh w(p, d, b, false);
-                for (int i = threadIdx.x; i < kChunk && k * kChunk + i < p.V; i += kThreads) {
-                    const double s = w.score(k * kChunk + i);
-                    if (s >= 0.0 && (v < 0 || s > score || (s == score && k * kChunk + i < v))) {
-                        score = s;
-                        v = k * kChunk + i;
-                    }
+        if (v < 0) {   // nothing is left of p - q: p itself
+            const Weigh w(p, d, b, false);
+            for (int k = threadIdx.x; k < p.V; k += kThreads) {
+                const double s = w.score(k);
+                if (s >= 0.0 && (v < 0 || s > score)) {
+                    score = s;
+                    v = k;
                 }
-                if (k == p.chunks - 1) ahead(score, v);
             }
+            ahead(score, v);
+        }
         chosen = v;
     } else if (c > 0) {
         return;
@@ -517,14 +522,15 @@ __global__ void __launch_bounds__(kThreads) verify_choose_kernel(const __grid_co
 
 struct Layout {
     size_t tickets, best, stats, total;
-    int chunks;
+    int chunks, laps;
 };
 Layout layout(int B, int T, int V, bool draft) {
     Layout L;
     L.chunks = (V + kChunk - 1) / kChunk;
+    L.laps = (V + kLap - 1) / kLap;
     L.tickets = kBehindZero;
     L.best = align_up(L.tickets + (size_t)B * 4, 256);
-    L.stats = align_up(L.best + (size_t)B * L.chunks * sizeof(Best), 256);
+    L.stats = align_up(L.best + (size_t)B * L.laps * sizeof(Best), 256);
     L.total = align_up(L.stats + (size_t)T * (draft ? 2 : 1) * L.chunks * sizeof(Stat), 256);
     return L;
 }
@@ -536,10 +542,10 @@ size_t verify_workspace_bytes(int B, int T, int V) { return layout(B, T, V, true
 cudaError_t launch_verify(const VerifyArgs &a, int B, int T, int V, void *ws, cudaStream_t s) {
     const Layout L = layout(B, T, V, a.draft != nullptr);
     const Params p{a.logits, a.draft, a.ls, a.ds, a.ns, a.drafts, a.cu, a.temperature, a.uniform, a.noise, a.tokens, a.accepted,
-                   B, T, V, L.chunks, reinterpret_cast<Ctrl *>(ws), ws_at<uint32_t>(ws, L.tickets), ws_at<Best>(ws, L.best), ws_at<Stat>(ws, L.stats)};
+                   B, T, V, L.chunks, L.laps, reinterpret_cast<Ctrl *>(ws), ws_at<uint32_t>(ws, L.tickets), ws_at<Best>(ws, L.best), ws_at<Stat>(ws, L.stats)};
     const cudaError_t err = launch_pdl(verify_stats_kernel, dim3((unsigned)((T > 0 ? T : 1) * (a.draft ? 2 : 1) * L.chunks)), kThreads, 0, s, p);
     if (err != cudaSuccess) return err;
-    return launch_pdl(verify_choose_kernel, dim3((unsigned)L.chunks, (unsigned)B), kThreads, 0, s, p);
+    return launch_pdl(verify_choose_kernel, dim3((unsigned)L.laps, (unsigned)B), kThreads, 0, s, p);
 }
 
 }  // namespace moe
