@@ -494,8 +494,8 @@ MOE_API int moe_kv4_attention_window(const uint16_t *q, moe_strides q_strides, m
  * nothing but -inf in a row of logits or draft logits, and a temperature that is
  * negative or not finite (the next token is then -1); a draft outside [0, V) (it is
  * refused, and takes nothing from p where draft_logits is NULL); offsets that do not
- * rise within [0, T] (brought into their range). Rows of tokens that no sequence
- * has are not written.
+ * rise within [0, T], anywhere (nothing is accepted, and there is no next token: -1).
+ * Rows of tokens that no sequence has are not written.
  *
  * ws: moe_verify_workspace_size() bytes under the rules of the MoE calls; it may
  * be one that they use.

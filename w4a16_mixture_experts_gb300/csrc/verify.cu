@@ -11,10 +11,12 @@
 // t = 0: accepted while x_i is the row's largest logit (the first of equals).
 //
 // What bounds it: every logit is read once (2 bytes) for the rows' largest values
-// and sums of exponentials, a row of each sequence and its noise once more. Two
+// and sums of exponentials, a row of each sequence and its noise once more. Three
 // launches: rows' statistics by chunks, over all rows at once (which row decides is
-// known only after them), then the decision and the race, by chunks of the
-// deciding row; the last CTA of a sequence to finish joins its chunks.
+// known only after them); the decision, a CTA a sequence; the race, by laps of the
+// deciding row, the last CTA of a sequence to finish joining them. (The decision in
+// every CTA of the race instead: 77 us for 32 sequences of 4 drafts and 248320
+// tokens; in the last CTA of a sequence's statistics: those took 44 us for 31.)
 //
 // The race is run in fp32, with bounds on each score (kSlack below). Where the
 // bounds leave more than one token, those are weighed again in 64 bits, as is a
@@ -31,6 +33,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kVecs = 8, kChunk = kThreads * 8 * kVecs;   // 16-byte loads of a thread and logits in a chunk of the statistics
+constexpr int kRacePerSm = 4;
 constexpr int kLapVecs = 4, kLap = kThreads * 8 * kLapVecs;   // ... and of the race
 static_assert(kThreads * kLap >= 1 << 20, "a thread a lap");
 constexpr float kLog2e = 1.4426950408889634f;
@@ -41,11 +44,12 @@ constexpr float kMinNoise = 1.17549435e-38f;
 constexpr float kSlack = 1.f / 65536.f;
 constexpr float kSlackAbs = 2.4e-38f;   // and what fp32 holds as zero
 
-struct Stat {       // of a chunk of a row
+struct alignas(16) Stat {       // of a chunk of a row
     float m, s;     // the largest logit, the sum of exp((l - m) / t): NaN where a logit is NaN or +inf
     int arg, pad;   // (t = 0) the first place of m
 };
 
+constexpr int kWritten = -2;
 struct Best {           // of a lap: the token ahead, and bounds on its score
     double low, high;
     int v, pad;         // v < 0: none has a weight
@@ -59,7 +63,8 @@ struct Params {
     int32_t *tokens, *accepted;
     int B, T, V, chunks, laps;
     Ctrl *ctrl;
-    uint32_t *tickets;   // [B], cleared by the first launch
+    uint32_t *tickets;   // [B]: CTAs of a sequence's race done; cleared with the decision
+    struct Decision *decisions;   // [B]
     Best *best;          // [B][laps]
     Stat *stats;         // [T][1 or 2][chunks]
 };
@@ -74,14 +79,10 @@ struct Rows {
     int r0, n;   // first row, rows
 };
 
+// Offsets that do not rise within [0, T] bound no rows.
 __device__ inline Rows rows_of(const Params &p, int b) {
     const int a = p.cu[b], e = p.cu[b + 1];
-    Rows r;
-    r.r0 = min(max(a, 0), p.T);
-    const int end = min(max(e, r.r0), p.T);
-    r.n = end - r.r0;
-    if (r.r0 != a || end != e) set_error(p.ctrl, MOE_ERR_DEVICE);
-    return r;
+    return a < 0 || e > p.T || e < a ? Rows{0, 0} : Rows{a, e - a};
 }
 
 // The sequence that row r belongs to, or -1; a whole warp calls it. 32 places at a time.
@@ -146,21 +147,120 @@ __device__ inline float warp_sum(float v) {
 // s * exp2((m - top) * rate), also where both are -inf and s is 0 (or NaN, which stays).
 __device__ inline float lowered(float s, float m, float top, float rate) { return m == top ? s : s * ex2((m - top) * rate); }
 
+struct Row {
+    float m, z;     // the largest logit, the sum of exp((l - m) / t)
+    int arg;        // (t = 0) the first place of m
+    bool bad;       // no distribution: a NaN, a +inf, nothing but -inf
+};
+
+// A whole warp calls it, a chunk a lane.
+__device__ inline Row row_stats(const Params &p, int r, int side, float rate) {
+    const Stat *st = p.stats + ((size_t)r * (p.draft ? 2 : 1) + side) * p.chunks;
+    const int lane = threadIdx.x & 31;
+    Row o{-INFINITY, 0.f, 0x7fffffff, false};
+    for (int c0 = 0; c0 < p.chunks; c0 += 32) {
+        const bool in = c0 + lane < p.chunks;
+        const float4 v = in ? __ldcg(reinterpret_cast<const float4 *>(st + c0 + lane)) : make_float4(-INFINITY, 0.f, __int_as_float(0x7fffffff), 0.f);
+        const Stat s{v.x, v.y, __float_as_int(v.z), 0};
+        const float m = fmaxf(o.m, warp_max(s.m));
+        const int arg = __reduce_min_sync(0xffffffffu, s.m == m ? s.arg : 0x7fffffff);
+        o.arg = m > o.m ? arg : min(o.arg, arg);
+        o.z = lowered(o.z, o.m, m, rate) + warp_sum(lowered(s.s, s.m, m, rate));
+        o.m = m;
+    }
+    o.bad = !(o.m > -INFINITY && o.z < INFINITY);
+    return o;
+}
+
+struct Decision {
+    int r0, n, a;       // rows of the sequence, accepted drafts
+    int chosen;         // the next token where the race does not decide (state 1)
+    int state, last;    // the deciding row is the last
+    int x;              // the draft that it refused: its q is 1 without draft logits (< 0: none)
+    float t, rate, mp, mq, zp, zq;
+};
+
+// In 64 bits: is u * q(x) < p(x)?
+__device__ __noinline__ bool accepts(float u, float l, float mp, float zp, bool has_q, float ld, float mq, float zq, float t) {
+    const double pv = exp(((double)l - mp) / t) / zp, qv = has_q ? exp(((double)ld - mq) / t) / zq : 1.0;
+    return (double)u * qv < pv;
+}
+
+struct Test {   // of a row's draft
+    Row p, q;
+    int x, stop, fault, last;
+};
+
+// What becomes of sequence b, which has rows: all threads call it, a row a warp.
+__device__ inline Decision decide(const Params &p, int b, const Rows &rows) {
+    __shared__ Test s_test[kThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Decision d{rows.r0, rows.n, 0, -1, 1, 0, -1, p.temperature ? p.temperature[b] : 1.f, 0.f, 0.f, 0.f, 1.f, 1.f};
+    const bool greedy = d.t == 0.f;
+    if (!(d.t >= 0.f && d.t < INFINITY)) {
+        if (threadIdx.x == 0) set_error(p.ctrl, MOE_ERR_DEVICE);
+        return d;
+    }
+    d.rate = greedy ? 1.f : rate_of(d.t);
+    for (int i0 = 0;; i0 += kThreads / 32) {
+        const int i = i0 + warp, r = rows.r0 + i;
+        Test t{{0.f, 1.f, 0, false}, {0.f, 1.f, 0, false}, -1, 1, 0, 0};
+        if (i < rows.n) {
+            t.last = i == rows.n - 1;
+            const bool has_q = p.draft && !greedy && !t.last;
+            const int x = t.last ? -1 : p.drafts[r];
+            const bool known = (unsigned)x < (unsigned)p.V;
+            const float l = known ? bf16_bits_to_f32(p.logits[r * p.ls + x]) : 0.f;
+            const float ld = known && has_q ? bf16_bits_to_f32(p.draft[r * p.ds + x]) : 0.f;
+            const float u = t.last ? 0.f : p.uniform[r];
+            t.p = row_stats(p, r, 0, d.rate);
+            if (has_q) t.q = row_stats(p, r, 1, d.rate);
+            t.x = t.last ? -1 : known ? x : -2;
+            t.fault = t.p.bad || t.q.bad;
+            if (!t.last && !t.fault && known) {
+                if (greedy) {
+                    t.stop = t.p.arg != x;
+                } else {
+                    const float pv = ex2((l - t.p.m) * d.rate) / t.p.z, uq = has_q ? u * (ex2((ld - t.q.m) * d.rate) / t.q.z) : u;
+                    if (fabsf(pv - uq) > 2.f * kSlack * (pv + fabsf(uq)) && fmaxf(pv, fabsf(uq)) > 1e-30f) t.stop = !(uq < pv);
+                    else t.stop = !accepts(u, l, t.p.m, t.p.z, has_q, ld, t.q.m, t.q.z, d.t);
+                }
+            }
+        }
+        if (i0) __syncthreads();
+        if (lane == 0) s_test[warp] = t;
+        __syncthreads();
+        int k = 0;
+        while (k < kThreads / 32 && !s_test[k].stop) ++k;
+        if (k == kThreads / 32) continue;
+        const Test &e = s_test[k];
+        d.a = i0 + k;
+        d.last = e.last;
+        d.x = e.x;
+        d.mp = e.p.m;
+        d.zp = e.p.z;
+        d.mq = e.q.m;
+        d.zq = e.q.z;
+        if ((e.fault || e.x == -2) && threadIdx.x == 0) set_error(p.ctrl, MOE_ERR_DEVICE);
+        d.state = e.fault || greedy;
+        d.chosen = e.fault ? -1 : e.p.arg;
+        return d;
+    }
+}
+
 __global__ void __launch_bounds__(kThreads) verify_stats_kernel(const __grid_constant__ Params p) {
     __shared__ float s_m[kThreads / 32], s_s[kThreads / 32];
     __shared__ int s_arg;
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b < p.B; b += kThreads) p.tickets[b] = 0;
-    if (p.T == 0) return;
     const int c = blockIdx.x % p.chunks, rw = blockIdx.x / p.chunks, sides = p.draft ? 2 : 1;
     const int side = rw / p.T, r = rw - side * p.T;
     const int b = sequence_of(p, r);
     if (b < 0) return;
+    const Rows rows = rows_of(p, b);
     const float t = p.temperature ? p.temperature[b] : 1.f;
-    if (side && (t == 0.f || r + 1 >= p.cu[b + 1])) return;   // not looked at
+    if (side && (t == 0.f || r == rows.r0 + rows.n - 1)) return;   // not looked at
     const float rate = t == 0.f ? 1.f : rate_of(t);
     const uint16_t *row = side ? p.draft + r * p.ds : p.logits + r * p.ls;
     uint4 v[kVecs];
@@ -235,106 +335,26 @@ __global__ void __launch_bounds__(kThreads) verify_stats_kernel(const __grid_con
     }
 }
 
-struct Row {
-    float m, z;     // the largest logit, the sum of exp((l - m) / t)
-    int arg;        // (t = 0) the first place of m
-    bool bad;       // no distribution: a NaN, a +inf, nothing but -inf
-};
-
-// A whole warp calls it, a chunk a lane.
-__device__ inline Row row_stats(const Params &p, int r, int side, float rate) {
-    const Stat *st = p.stats + ((size_t)r * (p.draft ? 2 : 1) + side) * p.chunks;
-    const int lane = threadIdx.x & 31;
-    Row o{-INFINITY, 0.f, 0x7fffffff, false};
-    for (int c0 = 0; c0 < p.chunks; c0 += 32) {
-        const bool in = c0 + lane < p.chunks;
-        const Stat s = in ? st[c0 + lane] : Stat{-INFINITY, 0.f, 0x7fffffff, 0};
-        const float m = fmaxf(o.m, warp_max(s.m));
-        const int arg = __reduce_min_sync(0xffffffffu, s.m == m ? s.arg : 0x7fffffff);
-        o.arg = m > o.m ? arg : min(o.arg, arg);
-        o.z = lowered(o.z, o.m, m, rate) + warp_sum(lowered(s.s, s.m, m, rate));
-        o.m = m;
-    }
-    o.bad = !(o.m > -INFINITY && o.z < INFINITY);
-    return o;
-}
-
-struct Decision {
-    int r0, n, a;       // rows of the sequence, accepted drafts
-    int chosen;         // the next token where the race does not decide (state 1)
-    int state, last;    // the deciding row is the last
-    int x;              // the draft that it refused: its q is 1 without draft logits (< 0: none)
-    float t, rate, mp, mq, zp, zq;
-};
-
-// In 64 bits: is u * q(x) < p(x)?
-__device__ __noinline__ bool accepts(float u, float l, float mp, float zp, bool has_q, float ld, float mq, float zq, float t) {
-    const double pv = exp(((double)l - mp) / t) / zp, qv = has_q ? exp(((double)ld - mq) / t) / zq : 1.0;
-    return (double)u * qv < pv;
-}
-
-struct Test {   // of a row's draft
-    Row p, q;
-    int x, stop, fault, last;
-};
-
-// What becomes of sequence b: all threads call it, a row a warp.
-__device__ inline Decision decide(const Params &p, int b) {
-    __shared__ Test s_test[kThreads / 32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// The decision for each sequence, and what follows where no race does. Offsets out of
+// order anywhere leave rows without statistics: then nothing is accepted.
+__global__ void __launch_bounds__(kThreads) verify_decide_kernel(const __grid_constant__ Params p) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int b = blockIdx.x;
+    bool order = true;
+    for (int i = threadIdx.x; i < p.B; i += kThreads) order &= p.cu[i] >= 0 && p.cu[i] <= p.cu[i + 1] && p.cu[i + 1] <= p.T;
+    order = __syncthreads_and(order);
     const Rows rows = rows_of(p, b);
-    Decision d{rows.r0, rows.n, 0, -1, 1, 0, -1, p.temperature ? p.temperature[b] : 1.f, 0.f, 0.f, 0.f, 1.f, 1.f};
-    const bool greedy = d.t == 0.f;
-    if (!(d.t >= 0.f && d.t < INFINITY)) {
-        if (rows.n > 0) set_error(p.ctrl, MOE_ERR_DEVICE);
-        return d;
+    Decision d{rows.r0, rows.n, 0, -1, 1, 0, -1, 0.f, 0.f, 0.f, 0.f, 1.f, 1.f};
+    if (!order && threadIdx.x == 0) set_error(p.ctrl, MOE_ERR_DEVICE);
+    if (order && rows.n > 0) d = decide(p, b, rows);
+    if (threadIdx.x == 0) {
+        p.decisions[b] = d;
+        p.tickets[b] = 0;
+        p.accepted[b] = d.a;
     }
-    if (rows.n == 0) return d;
-    d.rate = greedy ? 1.f : rate_of(d.t);
-    for (int i0 = 0;; i0 += kThreads / 32) {
-        const int i = i0 + warp, r = rows.r0 + i;
-        Test t{{0.f, 1.f, 0, false}, {0.f, 1.f, 0, false}, -1, 1, 0, 0};
-        if (i < rows.n) {
-            t.last = i == rows.n - 1;
-            const bool has_q = p.draft && !greedy && !t.last;
-            const int x = t.last ? -1 : p.drafts[r];
-            const bool known = (unsigned)x < (unsigned)p.V;
-            const float l = known ? bf16_bits_to_f32(p.logits[r * p.ls + x]) : 0.f;
-            const float ld = known && has_q ? bf16_bits_to_f32(p.draft[r * p.ds + x]) : 0.f;
-            const float u = t.last ? 0.f : p.uniform[r];
-            t.p = row_stats(p, r, 0, d.rate);
-            if (has_q) t.q = row_stats(p, r, 1, d.rate);
-            t.x = t.last ? -1 : known ? x : -2;
-            t.fault = t.p.bad || t.q.bad;
-            if (!t.last && !t.fault && known) {
-                if (greedy) {
-                    t.stop = t.p.arg != x;
-                } else {
-                    const float pv = ex2((l - t.p.m) * d.rate) / t.p.z, uq = has_q ? u * (ex2((ld - t.q.m) * d.rate) / t.q.z) : u;
-                    if (fabsf(pv - uq) > 2.f * kSlack * (pv + fabsf(uq)) && fmaxf(pv, fabsf(uq)) > 1e-30f) t.stop = !(uq < pv);
-                    else t.stop = !accepts(u, l, t.p.m, t.p.z, has_q, ld, t.q.m, t.q.z, d.t);
-                }
-            }
-        }
-        if (i0) __syncthreads();
-        if (lane == 0) s_test[warp] = t;
-        __syncthreads();
-        int k = 0;
-        while (k < kThreads / 32 && !s_test[k].stop) ++k;
-        if (k == kThreads / 32) continue;
-        const Test &e = s_test[k];
-        d.a = i0 + k;
-        d.last = e.last;
-        d.x = e.x;
-        d.mp = e.p.m;
-        d.zp = e.p.z;
-        d.mq = e.q.m;
-        d.zq = e.q.z;
-        if ((e.fault || e.x == -2) && threadIdx.x == 0) set_error(p.ctrl, MOE_ERR_DEVICE);
-        d.state = e.fault || greedy;
-        d.chosen = e.fault ? -1 : e.p.arg;
-        return d;
-    }
+    for (int i = threadIdx.x; i < rows.n; i += kThreads)   // (the race writes the one at d.a where it is run)
+        if (i != d.a || d.state) p.tokens[rows.r0 + i] = i < d.a ? p.drafts[rows.r0 + i] : i == d.a ? d.chosen : -1;
 }
 
 // The deciding row's values and what a token weighs in it.
@@ -398,35 +418,56 @@ __device__ inline Best race(const Weigh &w, int c) {
     const Decision &d = w.d;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, v0 = c * kLap + threadIdx.x * 8;
     const float lzp = -log2f(d.zp), lzq = -log2f(d.zq);
-    // bounds on a token's score; high < 0: no weight
-    auto bounds = [&](float l, float ld, float noise, int v, float &low, float &high) {
-        const float pv = ex2(fmaf(l - d.mp, d.rate, lzp)), qv = w.drow ? ex2(fmaf(ld - d.mq, d.rate, lzq)) : 0.f;
-        const float r = pv - qv, off = fmaf(kSlack, pv + qv, kSlackAbs), inv = __fdividef(1.f, Weigh::noise_of(noise));
-        low = (r - off) * inv;
-        high = r + off > 0.f && v != w.none && l > -INFINITY ? (r + off) * inv : -1.f;
-        if (v == w.none) low = 0.f;
-    };
+    const float2 m2 = make_float2(-d.mp, -d.mp), mq2 = make_float2(-d.mq, -d.mq), rate = make_float2(d.rate, d.rate);
+    const float2 zp = make_float2(lzp, lzp), zq = make_float2(lzq, lzq);
+    const float2 less = make_float2(1.f - kSlack, 1.f - kSlack), more = make_float2(1.f + kSlack, 1.f + kSlack);
+    const float2 neg_less = make_float2(kSlack - 1.f, kSlack - 1.f), neg_more = make_float2(-1.f - kSlack, -1.f - kSlack);
+    const float2 off = make_float2(kSlackAbs, kSlackAbs), neg_off = make_float2(-kSlackAbs, -kSlackAbs);
     float low = 0.f, high = -1.f;
+    // each(v, low, high) for pairs of tokens and bounds on their scores; high <= 0: no weight
     auto pass = [&](auto &&each) {
 #pragma unroll 2
         for (int i = 0; i < kLapVecs; ++i) {
             const int at = v0 + i * kThreads * 8;
             const uint4 l = load8(w.row, at, p.V), ld = w.drow ? load8(w.drow, at, p.V) : make_uint4(0, 0, 0, 0);
-            float x[8], y[8], e[8];
+            float e[8];
             noise8(w.noise, at, p.V, e);
-            unpack8(l, x);
-            unpack8(ld, y);
+            const uint32_t lw[4] = {l.x, l.y, l.z, l.w}, dw[4] = {ld.x, ld.y, ld.z, ld.w};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float lo, hi;
-                bounds(x[j], y[j], e[j], at + j, lo, hi);
-                each(at + j, lo, hi);
+            for (int j = 0; j < 4; ++j) {
+                float2 x = make_float2(__uint_as_float(lw[j] << 16), __uint_as_float(lw[j] & 0xffff0000u));
+                x = __ffma2_rn(__fadd2_rn(x, m2), rate, zp);
+                x = make_float2(ex2(x.x), ex2(x.y));
+                float2 lo = __ffma2_rn(x, less, neg_off), hi = __ffma2_rn(x, more, off);
+                if (w.drow) {
+                    float2 y = make_float2(__uint_as_float(dw[j] << 16), __uint_as_float(dw[j] & 0xffff0000u));
+                    y = __ffma2_rn(__fadd2_rn(y, mq2), rate, zq);
+                    y = make_float2(ex2(y.x), ex2(y.y));
+                    lo = __ffma2_rn(y, neg_more, lo);
+                    hi = __ffma2_rn(y, neg_less, hi);
+                }
+                const float2 inv = make_float2(__fdividef(1.f, Weigh::noise_of(e[2 * j])), __fdividef(1.f, Weigh::noise_of(e[2 * j + 1])));
+                lo = __fmul2_rn(lo, inv);
+                hi = __fmul2_rn(hi, inv);
+                if (w.none >> 1 == (at >> 1) + j) {   // (a token without weight)
+                    if (w.none & 1) lo.y = 0.f, hi.y = -1.f;
+                    else lo.x = 0.f, hi.x = -1.f;
+                }
+                each(at + 2 * j, lo, hi);
             }
         }
     };
-    pass([&](int, float lo, float hi) {
-        low = fmaxf(low, lo);
-        high = fmaxf(high, hi);
+    // the two highest bounds of the thread's tokens, and whose the first is
+    float second = -1.f;
+    int who = -1;
+    pass([&](int v, float2 lo, float2 hi) {
+        low = fmaxf(low, fmaxf(lo.x, lo.y));
+        second = fmaxf(second, fminf(high, hi.x));
+        who = hi.x > high ? v : who;
+        high = fmaxf(high, hi.x);
+        second = fmaxf(second, fminf(high, hi.y));
+        who = hi.y > high ? v + 1 : who;
+        high = fmaxf(high, hi.y);
     });
     low = warp_max(low);
     __syncthreads();
@@ -434,94 +475,86 @@ __device__ inline Best race(const Weigh &w, int c) {
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kThreads / 32; ++k) low = fmaxf(low, s_low[k]);
-    // who may be ahead of all
-    int count = 0;
-    Best o{0.0, 0.0, -1, 0};
-    if (high >= low)
-        pass([&](int v, float lo, float hi) {
-            if (hi < low) return;
-            ++count;
-            o = Best{fmaxf(lo, 0.f), hi, v, 0};
-        });
-    const int some = __syncthreads_count(count > 0), many = __syncthreads_or(count > 1);
-    if (some == 0) return Best{0.0, 0.0, -1, 0};
-    if (some == 1 && !many && low > 0.f) {   // one, and it has a weight
-        if (count == 1) p.best[blockIdx.y * (size_t)p.laps + c] = o;
-        o.v = -2;   // (written)
-        return o;
+    // who may be ahead of all: mostly one
+    const bool in = high >= low;
+    if (!__syncthreads_or(in)) return Best{0.0, 0.0, -1, 0};
+    const int some = __syncthreads_count(in), many = __syncthreads_or(second >= low);
+    if (some == 1 && !many && low > 0.f) {   // (and it has a weight)
+        if (in) p.best[blockIdx.y * (size_t)p.laps + c] = Best{low, high, who, 0};
+        return Best{0.0, 0.0, kWritten, 0};
     }
     double score = 0.0;
     int v = -1;
-    if (count > 0)
-        pass([&](int k, float, float hi) {
-            if (hi < low) return;
-            const double s = w.score(k);
-            if (s >= 0.0 && (v < 0 || s > score)) {
-                score = s;
-                v = k;
-            }
+    if (in)
+        pass([&](int k, float2, float2 hi) {
+            auto take = [&](int at, float h) {
+                if (h < low || at >= p.V) return;
+                const double s = w.score(at);
+                if (s >= 0.0 && (v < 0 || s > score)) {
+                    score = s;
+                    v = at;
+                }
+            };
+            take(k, hi.x);
+            take(k + 1, hi.y);
         });
     ahead(score, v);
     return Best{score, score, v, 0};
 }
 
-__global__ void __launch_bounds__(kThreads, 3) verify_choose_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, kRacePerSm) verify_race_kernel(const __grid_constant__ Params p) {
     __shared__ bool s_last;
     const int b = blockIdx.y, c = blockIdx.x;
     {   // (the noise on its way while the decision is made)
         const int v = c * kLap + threadIdx.x * 32;
-        if (v < p.V) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.noise + b * p.ns + v));
+        if (v < min((c + 1) * kLap, p.V)) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.noise + b * p.ns + v));
     }
     pdl_wait();
     pdl_launch_dependents();
-    const Decision d = decide(p, b);
-    int chosen = d.chosen;
-    if (d.state == 0) {
-        const bool residual = !d.last;
-        const Best o = race(Weigh(p, d, b, residual), c);
-        if (o.v != -2 && threadIdx.x == 0) p.best[(size_t)b * p.laps + c] = o;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            __threadfence();
-            s_last = atom_acq_rel_add_u32(p.tickets + b, 1) == (uint32_t)p.laps - 1;
-            __threadfence();
-        }
-        __syncthreads();
-        if (!s_last) return;
-        // ---- the laps' first ones against one another
-        double low = 0.0, score = 0.0;
-        int v = -1;
-        const Best *best = p.best + (size_t)b * p.laps;
-        for (int k = 0; k < p.laps; ++k) low = fmax(low, __ldcg(&best[k].low));
-        const Best mine = threadIdx.x < p.laps ? Best{0.0, __ldcg(&best[threadIdx.x].high), __ldcg(&best[threadIdx.x].v), 0} : Best{0.0, 0.0, -1, 0};
-        const bool in = mine.v >= 0 && mine.high >= low;
-        const int some = __syncthreads_count(in);
-        if (in) {
-            v = mine.v;
-            score = some > 1 ? Weigh(p, d, b, residual).score(v) : 0.0;
+    const Decision d = p.decisions[b];
+    if (d.state) return;
+    const Best o = race(Weigh(p, d, b, !d.last), c);
+    if (threadIdx.x == 0 && o.v != kWritten) p.best[(size_t)b * p.laps + c] = o;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        s_last = atom_acq_rel_add_u32(p.tickets + b, 1) == (uint32_t)p.laps - 1;
+        __threadfence();
+    }
+    __syncthreads();
+    if (!s_last) return;
+    // ---- the laps' first ones against one another
+    const Best *const best = p.best + (size_t)b * p.laps;
+    const bool there = threadIdx.x < p.laps;
+    const Best mine{there ? __ldcg(&best[threadIdx.x].low) : 0.0, there ? __ldcg(&best[threadIdx.x].high) : 0.0,
+                    there ? __ldcg(&best[threadIdx.x].v) : -1, 0};
+    double low = mine.low, score = 0.0;
+    int v = 0;
+    ahead(low, v);   // (the largest of the lower bounds)
+    const bool in = mine.v >= 0 && mine.high >= low;
+    const int some = __syncthreads_count(in);
+    v = -1;
+    if (in) {
+        v = mine.v;
+        score = some > 1 ? Weigh(p, d, b, !d.last).score(v) : 0.0;
+    }
+    ahead(score, v);
+    if (v < 0) {   // nothing is left of p - q: p itself
+        const Weigh w(p, d, b, false);
+        for (int k = threadIdx.x; k < p.V; k += kThreads) {
+            const double s = w.score(k);
+            if (s >= 0.0 && (v < 0 || s > score)) {
+                score = s;
+                v = k;
+            }
         }
         ahead(score, v);
-        if (v < 0) {   // nothing is left of p - q: p itself
-            const Weigh w(p, d, b, false);
-            for (int k = threadIdx.x; k < p.V; k += kThreads) {
-                const double s = w.score(k);
-                if (s >= 0.0 && (v < 0 || s > score)) {
-                    score = s;
-                    v = k;
-                }
-            }
-            ahead(score, v);
-        }
-        chosen = v;
-    } else if (c > 0) {
-        return;
     }
-    for (int i = threadIdx.x; i < d.n; i += kThreads) p.tokens[d.r0 + i] = i < d.a ? p.drafts[d.r0 + i] : i == d.a ? chosen : -1;
-    if (threadIdx.x == 0) p.accepted[b] = d.a;
+    if (threadIdx.x == 0) p.tokens[d.r0 + d.a] = v;
 }
 
 struct Layout {
-    size_t tickets, best, stats, total;
+    size_t tickets, decisions, best, stats, total;
     int chunks, laps;
 };
 Layout layout(int B, int T, int V, bool draft) {
@@ -529,7 +562,8 @@ Layout layout(int B, int T, int V, bool draft) {
     L.chunks = (V + kChunk - 1) / kChunk;
     L.laps = (V + kLap - 1) / kLap;
     L.tickets = kBehindZero;
-    L.best = align_up(L.tickets + (size_t)B * 4, 256);
+    L.decisions = align_up(L.tickets + (size_t)B * 4, 256);
+    L.best = align_up(L.decisions + (size_t)B * sizeof(Decision), 256);
     L.stats = align_up(L.best + (size_t)B * L.laps * sizeof(Best), 256);
     L.total = align_up(L.stats + (size_t)T * (draft ? 2 : 1) * L.chunks * sizeof(Stat), 256);
     return L;
@@ -542,10 +576,11 @@ size_t verify_workspace_bytes(int B, int T, int V) { return layout(B, T, V, true
 cudaError_t launch_verify(const VerifyArgs &a, int B, int T, int V, void *ws, cudaStream_t s) {
     const Layout L = layout(B, T, V, a.draft != nullptr);
     const Params p{a.logits, a.draft, a.ls, a.ds, a.ns, a.drafts, a.cu, a.temperature, a.uniform, a.noise, a.tokens, a.accepted,
-                   B, T, V, L.chunks, L.laps, reinterpret_cast<Ctrl *>(ws), ws_at<uint32_t>(ws, L.tickets), ws_at<Best>(ws, L.best), ws_at<Stat>(ws, L.stats)};
-    const cudaError_t err = launch_pdl(verify_stats_kernel, dim3((unsigned)((T > 0 ? T : 1) * (a.draft ? 2 : 1) * L.chunks)), kThreads, 0, s, p);
-    if (err != cudaSuccess) return err;
-    return launch_pdl(verify_choose_kernel, dim3((unsigned)L.laps, (unsigned)B), kThreads, 0, s, p);
+                   B, T, V, L.chunks, L.laps, reinterpret_cast<Ctrl *>(ws), ws_at<uint32_t>(ws, L.tickets), ws_at<Decision>(ws, L.decisions), ws_at<Best>(ws, L.best), ws_at<Stat>(ws, L.stats)};
+    cudaError_t err = T == 0 ? cudaSuccess : launch_pdl(verify_stats_kernel, dim3((unsigned)(T * (a.draft ? 2 : 1) * L.chunks)), kThreads, 0, s, p);
+    if (err == cudaSuccess) err = launch_pdl(verify_decide_kernel, dim3((unsigned)B), kThreads, 0, s, p);
+    if (err == cudaSuccess && T > 0) err = launch_pdl(verify_race_kernel, dim3((unsigned)L.laps, (unsigned)B), kThreads, 0, s, p);
+    return err;
 }
 
 }  // namespace moe
