@@ -453,7 +453,8 @@ MOE_API int moe_kv4_attention(const uint16_t *q, moe_strides q_strides, moe_kv4_
  * 16 keys, so the pages that lie wholly before the windows of a sequence's queries
  * of this call (first keys aside) may be gone: their entries in page_table are not
  * looked at. What else holds for moe_kv4_attention holds here, hidden keys counting
- * as those that a query does not see: whatever lies in them changes nothing.
+ * as those that a query does not see. What lies in keys that no query of a row tile
+ * sees (they share a run with keys that one does) changes no bit of the tile's rows.
  */
 MOE_API int moe_kv4_attention_window(const uint16_t *q, moe_strides q_strides, moe_kv4_cache cache,
                              const int32_t *page_table, int32_t max_pages, const int32_t *lens, const int32_t *cu_q,

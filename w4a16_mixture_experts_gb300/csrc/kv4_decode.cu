@@ -291,6 +291,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
     auto first_key = [&](int st) { return (kWindow ? gap.key_unit(st) : st) * kKeys; };
     // (a run that no row sees is not read: its page may be gone)
     auto in_reach = [&](int key) { return key < it.s.len && (!kWindow || key < p.sinks || key > low - 16); };
+    // (nor does a key that no row sees, of a run that is read, count for the exponent that the V scales share)
+    auto seen = [&](int key) { return kWindow ? key < tile_keys(it.s, p.G, R, it.qt) && (key < p.sinks || key >= low) : key < it.s.len; };
     auto page_of = [&](int st) {
         const int key = first_key(st) + run;
         return st < st1 && in_reach(key) ? ld_here(p.b.table + (size_t)it.b * p.b.max_pages + (key >> p.b.shift)) : -1;
@@ -450,7 +452,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, R>::kThreads, DecodeCfg<D, R>::kP
         copies_wait<0>();   // (K; V belongs to the next group)
         __syncwarp();
         {
-            const float fv = at0 != kNone && first_key(st) + tid < it.s.len ? fabsf(bf16_bits_to_f32(sh.scales[warp][0][1][lane])) : 0.f;
+            const float fv = at0 != kNone && seen(first_key(st) + tid) ? fabsf(bf16_bits_to_f32(sh.scales[warp][0][1][lane])) : 0.f;
             const uint32_t e = fv > 0.f && fv < INFINITY ? max(__float_as_uint(fv) >> 23, 1u) : 0u, top = __reduce_max_sync(0xffffffffu, e);
             if (lane == 0) sh.we[warp] = (int)top;
         }

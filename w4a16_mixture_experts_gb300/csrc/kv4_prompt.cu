@@ -645,6 +645,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
             auto first_key = [&](int st) { return (kWindow ? gap.key_unit(st) : st) * kKeys; };
             // (a run that no row sees is not read: its page may be gone)
             auto in_reach = [&](int key) { return key < len && (!kWindow || key < p.sinks || key > low - 16); };
+            // a key that no row sees, of a run that is read, is as one that is not there: it counts for no exponent,
+            // and what would be out of their range does not enter the products
+            const int end = kWindow ? tile_keys(it.s, p.G, kR, it.qt) : len;
+            auto seen = [&](int key) { return key < end && (!kWindow || key < p.sinks || key >= low); };
             auto page_of = [&](int st) {
                 const int key = first_key(st) + run;
                 return st < st1 && in_reach(key) ? ld_here(table + (key >> p.b.shift)) : -1;
@@ -685,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
 #pragma unroll
                 for (int i = 0; i < Cfg::kChunks; ++i) w[i] = lds_v4(raw + (lane * Cfg::kChunks + (i ^ turned(lane))) * 16);
                 const int key = first_key(st) + r;
-                const bool there = at0 != kNone && key < len;
+                const bool there = at0 != kNone && seen(key);
                 const uint16_t ks = there ? scales[slot][0][lane] : (uint16_t)0, vs = there ? scales[slot][1][lane] : (uint16_t)0;
                 __syncwarp();
                 slot = slot == 2 ? 0 : slot + 1;
@@ -700,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(Attn p) {
                 const bool bad = !finite_bits(ks) || !finite_bits(vs);
                 const float kf = bad ? 0.f : bf16_bits_to_f32(ks), vf = bad ? 0.f : bf16_bits_to_f32(vs);
                 // (a row of zeros in V lies far below the others: its key may have all the probability)
-                const int ke = exponent_of(kf, kNoExponent), ve = exponent_of(vf, in_reach(key & ~15) && key < len && !bad ? -100 : kNoExponent);
+                const int ke = exponent_of(kf, kNoExponent), ve = exponent_of(vf, seen(key) && !bad ? -100 : kNoExponent);
                 // (most stages change nothing: that is seen at the barrier alone. With four reductions a warp
                 // for each stage's own exponents the prompt chunk took 756 us, so 732; with the first stage's
                 // before the wait 850)
