@@ -447,8 +447,9 @@ __device__ inline Best race(const Weigh &w, int c) {
                     hi = __ffma2_rn(y, neg_less, hi);
                 }
                 const float2 inv = make_float2(__fdividef(1.f, Weigh::noise_of(e[2 * j])), __fdividef(1.f, Weigh::noise_of(e[2 * j + 1])));
+                // (above 2^126 the quotient is given as zero: there it is a lower bound alone)
                 lo = __fmul2_rn(lo, inv);
-                hi = __fmul2_rn(hi, inv);
+                hi = __fmul2_rn(hi, make_float2(fmaxf(inv.x, 0x1p-126f), fmaxf(inv.y, 0x1p-126f)));
                 if (w.none >> 1 == (at >> 1) + j) {   // (a token without weight)
                     if (w.none & 1) lo.y = 0.f, hi.y = -1.f;
                     else lo.x = 0.f, hi.x = -1.f;
