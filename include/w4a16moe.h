@@ -290,9 +290,9 @@ MOE_API int moe_w8a16_workspace_size(int32_t T, int32_t N, int32_t K, int32_t gs
  *   y[t][n] = sum_c x[t][c] * W[n][c]
  * x bf16 [T][K]; w_packed int32 [N][K/8]; scales bf16 [N][K/128]; y bf16 [T][N]
  * (output; must not overlap an input). K is a multiple of 128, at most 65536;
- * T <= 2^20. Codes enter the products exactly, sums are fp32 and each group's is
- * multiplied by its scale in fp32; y is rounded to bf16 once. A scale or a value
- * of x that is not finite reaches the values of y that it belongs to, and no others.
+ * T <= 2^20; N <= 2^31 - 256. Codes enter the products exactly, sums are fp32 and each
+ * group's is multiplied by its scale in fp32; y is rounded to bf16 once. A scale or a
+ * value of x that is not finite reaches the values of y that it belongs to, and no others.
  * The order of the sums depends on T, N, K and the device alone.
  * ws: moe_w4a16_workspace_size() bytes under the rules of the MoE calls (it may
  * be one that they use); a bounded wait that gave up sets MOE_ERR_TIMEOUT in it.

@@ -343,7 +343,7 @@ int moe_w4a16_linear(const uint16_t *x, const int32_t *w_packed, const uint16_t 
 
 int moe_w4a16_workspace_size(int32_t T, int32_t N, int32_t K, size_t *bytes) {
     if (!bytes || T < 0 || N < 0 || K <= 0) return MOE_ERR_INVALID_ARG;
-    if (K % kGroup || T > (1 << 20) || K > 65536) return MOE_ERR_UNSUPPORTED;
+    if (K % kGroup || T > (1 << 20) || K > 65536 || N > INT32_MAX - 255) return MOE_ERR_UNSUPPORTED;   // (rows of whole CTAs fit 32 bits)
     *bytes = w4a16_workspace_bytes(T, N, K);
     return MOE_OK;
 }
