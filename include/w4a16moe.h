@@ -293,9 +293,9 @@ MOE_API int moe_w8a16_workspace_size(int32_t T, int32_t N, int32_t K, int32_t gs
  * T <= 2^20; N <= 2^31 - 256. Codes enter the products exactly, sums are fp32 and each
  * group's is multiplied by its scale in fp32; y is rounded to bf16 once. A scale or a
  * value of x that is not finite reaches the values of y that it belongs to, and no others.
- * The order of the sums depends on T, N, K and the device alone.
- * ws: moe_w4a16_workspace_size() bytes under the rules of the MoE calls (it may
- * be one that they use); a bounded wait that gave up sets MOE_ERR_TIMEOUT in it.
+ * Each value of y is summed in one order, whatever T and N.
+ * ws: moe_w4a16_workspace_size() bytes, reserved: the call neither reads nor writes
+ * them (it may be a workspace of the MoE calls).
  * T = 0 or N = 0 return MOE_OK with nothing enqueued.
  */
 MOE_API int moe_w4a16_linear(const uint16_t *x, const int32_t *w_packed, const uint16_t *scales, uint16_t *y, int32_t T,

@@ -693,9 +693,9 @@ def moe_w4a16_workspace_size(T: int, N: int, K: int) -> int:
 
 def moe_w4a16_linear(x, w_packed, scales, y=None, ws=None, stream=None):
     """bf16 y [T, N] = x . W^T for INT4 weights in the experts' storage (moe_quantize_int4's): w_packed
-    int32 [N, K/8] (q + 8, eight to a word, lowest nibble first), scales bf16 [N, K/128]. ws: a zeroed
-    uint8 tensor of moe_w4a16_workspace_size bytes (allocated here when not given), whose error word
-    moe_check_device_error reads."""
+    int32 [N, K/8] (q + 8, eight to a word, lowest nibble first), scales bf16 [N, K/128]. ws: a
+    uint8 tensor of moe_w4a16_workspace_size bytes (allocated here when not given); the call neither reads
+    nor writes it."""
     if stream is not None and (y is None or ws is None):
         with _made_on(stream):
             return moe_w4a16_linear(x, w_packed, scales, y, ws)
@@ -707,9 +707,8 @@ def moe_w4a16_linear(x, w_packed, scales, y=None, ws=None, stream=None):
     if y is None:
         y = torch.empty(T, N, dtype=_BF16, device=x.device)
     yp, _ = _mat(y, "y", _BF16, T, N)
-    if ws is None:   # for this call alone: of what the call leaves zero it uses the control block only
+    if ws is None:   # (nothing is kept in it)
         ws = torch.empty(moe_w4a16_workspace_size(T, N, K), dtype=torch.uint8, device=x.device)
-        ws[:256].zero_()
     _check(lib().moe_w4a16_linear(xp, wp, sp, yp, T, N, K, *_ws_bytes(ws), _stream(stream)), "moe_w4a16_linear")
     return y
 
