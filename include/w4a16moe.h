@@ -291,8 +291,10 @@ MOE_API int moe_w8a16_workspace_size(int32_t T, int32_t N, int32_t K, int32_t gs
  * x bf16 [T][K]; w_packed int32 [N][K/8]; scales bf16 [N][K/128]; y bf16 [T][N]
  * (output; must not overlap an input). K is a multiple of 128, at most 65536;
  * T <= 2^20; N <= 2^31 - 256. Codes enter the products exactly, sums are fp32 and each
- * group's is multiplied by its scale in fp32; y is rounded to bf16 once. A scale or a
- * value of x that is not finite reaches the values of y that it belongs to, and no others.
+ * group's is multiplied by its scale in fp32; y is rounded to bf16 once. (A group's sum
+ * is formed before its scale: it is in range where |x| <= 2^117, and may pass to an
+ * infinity above that, whatever the scale.) A scale or a value of x that is not finite
+ * reaches the values of y that it belongs to, and no others.
  * Each value of y is summed in one order, whatever T and N.
  * ws: moe_w4a16_workspace_size() bytes, reserved: the call neither reads nor writes
  * them (it may be a workspace of the MoE calls).

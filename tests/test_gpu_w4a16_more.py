@@ -43,3 +43,18 @@ def test_a_workspace_is_left_as_it_is():
     ws = torch.full((512,), 7, dtype=torch.uint8, device="cuda")
     moe.moe_w4a16_linear(x, w, torch.ones(17, 1, device="cuda").bfloat16(), ws=ws)
     assert (ws == 7).all()
+
+
+@pytest.mark.parametrize("T", [1, 9])
+def test_the_largest_values_whose_sums_are_in_range(T):
+    # |x| <= 2^117: a group's sum is 128 x 8 x 2^117 = 2^127 at most; scales bring it back
+    K, N = 256, 24
+    x = torch.full((T, K), 2.0 ** 117, device="cuda").bfloat16()
+    w = torch.zeros(N, K // 8, dtype=torch.int32, device="cuda")    # every code -8
+    s = torch.full((N, K // 128), 2.0 ** -120, device="cuda").bfloat16()
+    assert (moe.moe_w4a16_linear(x, w, s) == -2.0 ** 8).all()
+    x[:, 128:] = -x[:, 128:]
+    assert (moe.moe_w4a16_linear(x, w, s) == 0).all()
+    # and from the other end: values of 2^-110, scales of 2^100
+    y = moe.moe_w4a16_linear(torch.full((T, K), 2.0 ** -110, device="cuda").bfloat16(), w, torch.full((N, 2), 2.0 ** 100, device="cuda").bfloat16())
+    assert (y == -2.0).all()
