@@ -99,3 +99,16 @@ def test_a_cache_that_was_filled_from_the_window_on(nq):
         assert ((got[0].double() - want).abs() <= tol).all() and ((got[1].double() - z).abs() <= ltol).all()
         for t, old in zip(tensors, kept):
             t[page, :, off] = old
+
+
+def test_windows_past_32_bits_hide_nothing_and_negative_ones_are_refused():
+    g = _gen(8)
+    q, cache, table, lens, nqs = _case(g, 2, 4, 64, 16, [3], [300])
+    want = _run(q, cache, table, lens, nqs, 2 ** 31 - 1, 0)
+    for window, sinks in ((2 ** 32 + 5, 0), (2 ** 32, 0), (2 ** 40, 0), (5, 2 ** 32 + 1), (5, 2 ** 33)):
+        got = _run(q, cache, table, lens, nqs, window, sinks)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), (window, sinks)
+    for window, sinks in ((5 - 2 ** 32, 0), (0, 0), (5, 1 - 2 ** 32), (5, -1)):
+        with pytest.raises(moe.MoeError) as e:
+            _run(q, cache, table, lens, nqs, window, sinks)
+        assert e.value.status == 1
