@@ -669,8 +669,9 @@ def _attention(q, cache, page_table, lens, cu_q, max_q, scale, out, lse, ws, str
     if window is None:
         _check(lib().moe_kv4_attention(*args, *rest), "moe_kv4_attention")
     else:
-        # (the C call counts in 32 bits, past which nothing is hidden; what is below its range stays below it)
-        window, sinks = min(max(window, -1), 2 ** 31 - 1), min(max(sinks, -1), 2 ** 31 - 1)
+        if not (0 <= window <= 0x7FFFFFFF and 0 <= sinks <= 0x7FFFFFFF):
+            # the C call counts in 32 bits, past which nothing is hidden; what is below its range stays below it
+            window, sinks = min(max(window, -1), 0x7FFFFFFF), min(max(sinks, -1), 0x7FFFFFFF)
         _check(lib().moe_kv4_attention_window(*args, window, sinks, *rest), "moe_kv4_attention_window")
     return out if lse is None else (out, lse)
 
