@@ -488,7 +488,9 @@ MOE_API int moe_kv4_attention_window(const uint16_t *q, moe_strides q_strides, m
  * logits, draft_logits bf16 [T][V] with rows `stride` values apart (a multiple of
  * 8); uniform f32 [T]; noise f32 [B][V], rows noise_stride (a multiple of 4)
  * apart. V <= 2^20, T <= 65536, B <= 4096. A logit of -inf is a token of
- * probability zero. noise below 2^-126 (NaN too) counts as 2^-126.
+ * probability zero (so that a row's top k or top p alone are sampled where the
+ * caller writes -inf elsewhere; draft_logits are those that the drafts were drawn
+ * from). noise below 2^-126 (NaN too) counts as 2^-126.
  *
  * Whatever is compared is compared in fp32 where bounds on its error leave no doubt,
  * and else in 64 bits, the rows' sums included: the result is that of the definition in

@@ -23,7 +23,7 @@ struct SmemAttr {
     int bytes;
     bool done[kMaxDevices];
 };
-constexpr int kMaxSmemKernels = 64;   // kernels that raise their shared-memory limit (30 today)
+constexpr int kMaxSmemKernels = 64;   // kernels that raise their shared-memory limit (28 today)
 SmemAttr g_attrs[kMaxSmemKernels];
 int g_nattrs = 0;
 std::mutex g_attrs_mu;   // callers may launch from several host threads

@@ -7,6 +7,11 @@
 // A code is exact in bf16, so the inner sums' products are exact and they add up
 // in fp32; a scale multiplies its group's sum in fp32: nothing is rounded to
 // fewer bits before y.
+//
+// A first form for every T: what bounds it is L1, from which every warp takes x again
+// (90% busy at 4 x 248320 x 2560, 84 us of a floor of 49; 99.7% at 4001 x 5121 x 4096,
+// 1552 us of 85), and where few rows leave SMs idle, each load's latency (7 x 2560 x
+// 10240: 35 us of 2). K is not split, and nothing is loaded ahead.
 #include "step_kernels.cuh"
 
 namespace moe {
