@@ -33,3 +33,9 @@ def test_the_largest_number_of_rows(L):
     blocks = (N + 15) // 16
     last = (blocks + 7) // 8 * 8 - 1
     assert N + 15 < 2 ** 31 and last * 16 + 7 + 8 < 2 ** 31
+
+
+def test_a_workspace_for_the_largest_batch_does_for_smaller_ones(L):
+    for N, K in [(5120, 2560), (320, 10240), (2560, 640), (17, 65536)]:
+        sizes = [moe.moe_w4a16_workspace_size(T, N, K) for T in (0, 1, 2, 4, 8, 9, 16, 40, 64, 100, 128, 129, 500, 4096, 1 << 20)]
+        assert sizes == sorted(sizes)
